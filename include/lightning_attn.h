@@ -414,6 +414,147 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
                                             void* workspace, size_t workspace_bytes, la_stream_t stream);
 
 /*
+ * Gated linear recurrence, channel by channel: the element-wise relative of the recurrence
+ * above, with a forget gate instead of a feature map.  The pages have no counterpart: layers
+ * of this kind stand beside the lightning layers in recurrent and hybrid models and share
+ * their life: a long prefill that ends in a small state, packed batches, one-token steps
+ * and a backward pass through the carried state.  Per sequence and channel, t = 1 .. T:
+ *   a_t = sigmoid(f_t),   b_t = x_t (PLAIN) or (1 - a_t) x_t (TIED),
+ *   h_t = a_t h_{t-1} + b_t,   h_0 = state_in (zeros if NULL),   out_t = h_t.
+ * Gates, products of gates and states are held in fp32; out is rounded once, from the fp32
+ * state.  The time axis is cut into blocks of rows that are worked on at the same time, so
+ * the result depends on where a sequence starts in the packed rows by fp32 rounding only; it
+ * is the same for every call with the same arguments.
+ *
+ *   x, f, out    [B, T, W] dtype (x and f read only; out may not alias them).
+ *   state_in     fp32 [B, W] initial state per sequence, or NULL for zeros.
+ *   state_out    fp32 [B, W] final state, or NULL.  May be state_in (in place).
+ *   checkpoints  fp32 [ceil(B*T / LA_RECURRENCE_CHECKPOINT_ROWS), W], or NULL: written with
+ *                the fp32 state that each LA_RECURRENCE_CHECKPOINT_ROWS-th packed row starts
+ *                from, for lightning_attn_gated_recurrence_backward.
+ *   B, T, W      B >= 1, T >= 0 (T == 0: no output; state_out = state_in or zeros), W >= 1.
+ *                Rows whose bytes are a multiple of 16 are read as 16-byte vectors; others
+ *                element by element (slower, same results).
+ *   workspace    device scratch of >= lightning_attn_gated_recurrence_workspace_size bytes,
+ *                256-byte aligned, its first 256 bytes (the error record, as for the
+ *                prefill) zero before its first use.
+ * f = +inf keeps the state (a = 1), f = -inf drops it (a = 0).  A NaN, or a state that left
+ * the fp32 range, stays in its own channel of its own sequence (an infinity may become NaN).
+ * Returns LA_OK after enqueueing, or an error status with nothing enqueued.
+ */
+typedef enum { LA_INPUT_PLAIN = 0, LA_INPUT_TIED = 1 } la_input_mode;
+
+#define LA_RECURRENCE_CHECKPOINT_ROWS 128
+
+LA_API la_status lightning_attn_gated_recurrence(const void* x, const void* f, void* out, const float* state_in,
+                                                 float* state_out, float* checkpoints, int B, int T, int W,
+                                                 la_dtype dtype, la_input_mode input_mode, void* workspace,
+                                                 size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * The gated recurrence over N packed sequences (cu_seqlens DEVICE int32 [N + 1] as for
+ * lightning_attn_prefill_varlen; x, f, out [total_tokens, W]; states fp32 [N, W]).  Empty
+ * sequences are allowed (state_out = state_in or zeros); rows behind cu_seqlens[N] are left
+ * as they were.  Violations found on the device are reported by lightning_attn_check.
+ */
+LA_API la_status lightning_attn_gated_recurrence_varlen(const void* x, const void* f, void* out,
+                                                        const float* state_in, float* state_out,
+                                                        float* checkpoints, const int* cu_seqlens, int num_seqs,
+                                                        int total_tokens, int W, la_dtype dtype,
+                                                        la_input_mode input_mode, void* workspace,
+                                                        size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * One token for each of B sequences: x, f, out [B, W]; state fp32 [B, W], updated IN PLACE.
+ * Needs no workspace and allocates nothing.  Other arguments as above.
+ */
+LA_API la_status lightning_attn_gated_recurrence_step(const void* x, const void* f, void* out, float* state, int B,
+                                                      int W, la_dtype dtype, la_input_mode input_mode,
+                                                      la_stream_t stream);
+
+/*
+ * Backward of lightning_attn_gated_recurrence: with G_t the gradient reaching h_t,
+ *   G_T = dout_T + dstate_out,   G_t = dout_t + a_{t+1} G_{t+1},
+ *   PLAIN: dx_t = G_t,             df_t = G_t a_t (1 - a_t) h_{t-1},
+ *   TIED:  dx_t = (1 - a_t) G_t,   df_t = G_t a_t (1 - a_t) (h_{t-1} - x_t),
+ *   dstate_in = a_1 G_1  (T == 0: dstate_out or zeros).
+ * h is recomputed in fp32 block by block from `checkpoints`, so that the rounded out is
+ * not needed and one tensor less is read.
+ *   x, f         [B, T, W] dtype, the forward's inputs; dout [B, T, W] dtype.
+ *   dx, df       [B, T, W] dtype, written (none may alias an input or the other).
+ *   state_in     fp32 [B, W], the forward's initial state, or NULL (zeros).
+ *   dstate_out   fp32 [B, W], the gradient reaching the final state, or NULL (zeros).
+ *   dstate_in    fp32 [B, W], written, or NULL.  May be dstate_out (in place).
+ *   checkpoints  as the forward of the same x, f, state_in and input_mode wrote them, or
+ *                NULL: they are recomputed (one more read of x and f).
+ *   workspace    >= lightning_attn_gated_recurrence_workspace_size(..., backward = 1) bytes.
+ */
+LA_API la_status lightning_attn_gated_recurrence_backward(const void* x, const void* f, const void* dout, void* dx,
+                                                          void* df, const float* state_in, const float* dstate_out,
+                                                          float* dstate_in, const float* checkpoints, int B, int T,
+                                                          int W, la_dtype dtype, la_input_mode input_mode,
+                                                          void* workspace, size_t workspace_bytes,
+                                                          la_stream_t stream);
+
+/* Backward of lightning_attn_gated_recurrence_varlen (layouts as there). */
+LA_API la_status lightning_attn_gated_recurrence_backward_varlen(
+    const void* x, const void* f, const void* dout, void* dx, void* df, const float* state_in,
+    const float* dstate_out, float* dstate_in, const float* checkpoints, const int* cu_seqlens, int num_seqs,
+    int total_tokens, int W, la_dtype dtype, la_input_mode input_mode, void* workspace, size_t workspace_bytes,
+    la_stream_t stream);
+
+/*
+ * Workspace bytes of the gated recurrence's calls over num_seqs sequences (B, or N) of
+ * total_tokens packed rows (B * T) of W channels; backward: 0 for the forward calls, 1 for
+ * the backward ones (which also serves the forward).  0 on invalid arguments.
+ */
+LA_API size_t lightning_attn_gated_recurrence_workspace_size(int num_seqs, int total_tokens, int W, la_dtype dtype,
+                                                             int backward);
+
+/*
+ * Layer norm over rows of W values, with the residual addition in front of it.  The pages
+ * have no counterpart (their layers' own norm is the output transform's RMSNorm): it is the
+ * norm with a mean and a bias that a layer's input passes.
+ *   s = x + residual,   y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias,
+ * var the mean of the squared deviations.  Sums are fp32; the deviations are taken from the
+ * mean before they are squared; y comes from the unrounded s.
+ *   x, out       [rows, W] dtype; out may be x or residual (in place).
+ *   residual     [rows, W] dtype, or NULL (s = x).
+ *   sum_out      [rows, W] dtype, or NULL: s, rounded to dtype (the residual stream that goes
+ *                on).  May be x or residual (in place), not out.
+ *   weight, bias fp32 [W], or NULL (ones, zeros).
+ *   W            1 <= W <= 16384 (beyond: LA_ERR_UNSUPPORTED); rows >= 0; eps > 0.  Rows whose
+ *                bytes are a multiple of 16 are read as 16-byte vectors, others element by
+ *                element (slower, same results).
+ */
+LA_API la_status lightning_attn_layer_norm(const void* x, const void* residual, const float* weight,
+                                           const float* bias, void* out, void* sum_out, int rows, int W,
+                                           la_dtype dtype, float eps, la_stream_t stream);
+
+/*
+ * Backward of lightning_attn_layer_norm.  With z = (s - mean) r, r = 1/sqrt(var(s) + eps)
+ * (recomputed from s) and g = dout * weight:
+ *   dx = r (g - mean(g) - z mean(g z)) + dsum,   dweight = sum dout z,   dbias = sum dout
+ * (dx is the gradient of both x and residual; the sums over the rows run in a fixed order).
+ *   s            [rows, W] dtype: the forward's sum_out, or its x where it had no residual.
+ *   dout         [rows, W] dtype.
+ *   dsum         [rows, W] dtype, the gradient reaching sum_out, or NULL.
+ *   dx           [rows, W] dtype, written; may be s, dout or dsum (in place).
+ *   dweight, dbias  fp32 [W], written (zeros for rows == 0), or NULL.
+ *   workspace    needed iff dweight or dbias is given: >= lightning_attn_layer_norm_workspace_size
+ *                bytes, 256-byte aligned.
+ * Other arguments as the forward.
+ */
+LA_API la_status lightning_attn_layer_norm_backward(const void* s, const void* dout, const void* dsum,
+                                                    const float* weight, void* dx, float* dweight, float* dbias,
+                                                    int rows, int W, la_dtype dtype, float eps, void* workspace,
+                                                    size_t workspace_bytes, la_stream_t stream);
+
+/* Workspace bytes of lightning_attn_layer_norm_backward (0 on invalid arguments; query with
+ * the target device current). */
+LA_API size_t lightning_attn_layer_norm_workspace_size(int rows, int W);
+
+/*
  * Workspace bytes needed by one call (0 on invalid arguments).
  *   op == LA_OP_PREFILL:         B_or_N = B, T_or_max = T, total_tokens ignored.
  *   op == LA_OP_PREFILL_VARLEN:  B_or_N = N, T_or_max = max_seqlen, total_tokens.
@@ -444,7 +585,7 @@ LA_API const char* lightning_attn_status_string(la_status s);
 
 /* Name of the kernel path the last successful call on this thread selected (diagnostic):
  * "tcgen05", "tcgen05+chunks", "tcgen05+norm", "tcgen05+norm+chunks", "simt", "decode",
- * "mixed", "tcgen05-state". */
+ * "mixed", "tcgen05-state", "recurrence", "recurrence-step", "recurrence-backward". */
 LA_API const char* lightning_attn_last_path(void);
 
 #ifdef __cplusplus

@@ -7,8 +7,11 @@ ranks) and is differentiable in q, k, v, g, state_in and the norm weight: its ba
 one `lightning_attn_backward` call (the gradient reaching `state_out`, when the final state
 feeds later computation, is passed to it as dstate_out).  When gradients are
 needed in a norm mode, the forward runs the prefill in raw mode and then the output
-transform, keeping the raw output y, which saves the backward its recompute of y.  This
-module only orders the library calls and allocates their outputs; every computation runs
+transform, keeping the raw output y, which saves the backward its recompute of y.
+
+`gated_recurrence`, `gated_recurrence_varlen` and `layer_norm` are the differentiable forms of
+`lightning_attn_gated_recurrence[_varlen]` and `lightning_attn_layer_norm`, the backward of
+each one call of the library's.  This module only orders the library calls and allocates their outputs; every computation runs
 in the library's kernels.
 """
 from __future__ import annotations
@@ -210,3 +213,99 @@ def lightning_attention_sequence_parallel(q, k, v, g=None, state0=None, norm_wei
         norm_weight = norm_weight.float().contiguous()
     return _SequenceParallelLightningAttention.apply(q, k, v, g, state0, norm_weight, rank, all_gather, block_size,
                                                      phi, mode, eps)
+
+
+class _GatedRecurrence(torch.autograd.Function):
+    """x, f [B, T, W] (cu_seqlens None) or packed [total, W]."""
+
+    @staticmethod
+    def forward(ctx, x, f, state_in, cu_seqlens, input_mode):
+        ctx.set_materialize_grads(False)
+        x, f = x.contiguous(), f.contiguous()
+        W = x.shape[-1]
+        tokens = x.shape[0] if cu_seqlens is not None else x.shape[0] * x.shape[1]
+        n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        out = torch.empty_like(x)
+        state_out = torch.empty((n, W), dtype=torch.float32, device=x.device)
+        s_in = None if state_in is None else state_in.detach().contiguous()
+        saved = la.new_recurrence_checkpoints(tokens, W, x.device) if any(ctx.needs_input_grad) else None
+        ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x)), x.device)
+        if cu_seqlens is None:
+            la.lightning_attn_gated_recurrence(x, f, out, s_in, state_out, saved, input_mode, ws)
+        else:
+            la.lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, s_in, state_out, saved, input_mode, ws)
+        ctx.save_for_backward(x, f, s_in, cu_seqlens, saved)
+        ctx.cfg = (n, tokens, input_mode)
+        return out, state_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dstate_out):
+        x, f, s_in, cu, saved = ctx.saved_tensors
+        n, tokens, input_mode = ctx.cfg
+        W = x.shape[-1]
+        dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype).contiguous()
+        ds_out = None if dstate_out is None else dstate_out.float().contiguous()
+        dx, df = torch.empty_like(x), torch.empty_like(f)
+        ds_in = torch.empty((n, W), dtype=torch.float32, device=x.device) if ctx.needs_input_grad[2] else None
+        ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x), True),
+                              x.device)
+        if cu is None:
+            la.lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, s_in, ds_out, ds_in, saved, input_mode, ws)
+        else:
+            la.lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu, s_in, ds_out, ds_in, saved,
+                                                               input_mode, ws)
+        return dx, df, ds_in, None, None
+
+
+def gated_recurrence(x, f, state_in=None, input_mode: int = la.LA_INPUT_TIED):
+    """Differentiable gated recurrence h_t = a_t h_{t-1} + b_t, a = sigmoid(f), b = x or (1 - a) x:
+    x, f [B, T, W]; state_in fp32 [B, W] or None.  Returns (out [B, T, W], state_out fp32 [B, W])."""
+    return _GatedRecurrence.apply(x, f, state_in, None, input_mode)
+
+
+def gated_recurrence_varlen(x, f, cu_seqlens, state_in=None, input_mode: int = la.LA_INPUT_TIED):
+    """Differentiable gated recurrence over packed sequences: x, f [total, W]; cu_seqlens int32
+    device [N + 1] with cu_seqlens[N] == total; state_in fp32 [N, W] or None.  Returns
+    (out [total, W], state_out fp32 [N, W])."""
+    return _GatedRecurrence.apply(x, f, state_in, cu_seqlens, input_mode)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        ctx.set_materialize_grads(False)
+        x = x.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        weight = None if weight is None else weight.detach()
+        out = torch.empty_like(x)
+        s = None if residual is None else torch.empty_like(x)
+        la.lightning_attn_layer_norm(x, out, residual=residual, sum_out=s, weight=weight,
+                                     bias=None if bias is None else bias.detach(), eps=eps)
+        ctx.save_for_backward(x if s is None else s, weight)
+        ctx.eps = eps
+        return out if s is None else (out, s)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dsum=None):
+        s, weight = ctx.saved_tensors
+        W = s.shape[-1]
+        need = ctx.needs_input_grad
+        dout = torch.zeros_like(s) if dout is None else dout.to(s.dtype).contiguous()
+        dsum = None if dsum is None else dsum.to(s.dtype).contiguous()
+        dx = torch.empty_like(s)
+        dw, db = (torch.empty(W, dtype=torch.float32, device=s.device) if n else None for n in need[1:3])
+        ws = None
+        if need[1] or need[2]:
+            ws = la.new_workspace(la.lightning_attn_layer_norm_workspace_size(s.numel() // W, W), s.device)
+        la.lightning_attn_layer_norm_backward(s, dout, dx, dsum=dsum, weight=weight, dweight=dw, dbias=db,
+                                              eps=ctx.eps, workspace=ws)
+        return dx if need[0] else None, dw, db, dx if need[3] else None, None
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5):
+    """Differentiable layer norm of x (+ residual) over the last axis: x, residual [..., W]; weight,
+    bias [W] or None.  Returns out, or (out, x + residual) where a residual is given."""
+    weight, bias = (None if t is None else t.float().contiguous() for t in (weight, bias))
+    return _LayerNorm.apply(x, weight, bias, residual, eps)

@@ -20,6 +20,8 @@ LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_E
 LA_F32, LA_BF16 = 0, 1
 LA_OUT_RAW, LA_OUT_RMSNORM, LA_OUT_RMSNORM_GATE = 0, 1, 2
 LA_PHI_SILU, LA_PHI_IDENTITY = 0, 1
+LA_INPUT_PLAIN, LA_INPUT_TIED = 0, 1
+LA_RECURRENCE_CHECKPOINT_ROWS = 128
 (LA_OP_PREFILL, LA_OP_PREFILL_VARLEN, LA_OP_DECODE, LA_OP_MIXED, LA_OP_BACKWARD, LA_OP_BACKWARD_VARLEN,
  LA_OP_PREFILL_ZNORM, LA_OP_PREFILL_ZNORM_VARLEN, LA_OP_CHUNK_STATE, LA_OP_OUTPUT_TRANSFORM_BACKWARD) = range(10)
 
@@ -39,6 +41,15 @@ EXPORTED = (
     "lightning_attn_chunk_state",
     "lightning_attn_output_transform",
     "lightning_attn_output_transform_backward",
+    "lightning_attn_gated_recurrence",
+    "lightning_attn_gated_recurrence_varlen",
+    "lightning_attn_gated_recurrence_step",
+    "lightning_attn_gated_recurrence_backward",
+    "lightning_attn_gated_recurrence_backward_varlen",
+    "lightning_attn_gated_recurrence_workspace_size",
+    "lightning_attn_layer_norm",
+    "lightning_attn_layer_norm_backward",
+    "lightning_attn_layer_norm_workspace_size",
     "lightning_attn_workspace_size",
     "lightning_attn_check",
     "lightning_attn_status_string",
@@ -77,6 +88,17 @@ def _load():
                                               f32, vp, vp, sz, vp, vp]
     lib.lightning_attn_state_prefix.argtypes = [vp, i32, i32, vp, vp, i32, i32, vp]
     lib.lightning_attn_chunk_state.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+    lib.lightning_attn_gated_recurrence.argtypes = [vp] * 6 + [i32] * 5 + [vp, sz, vp]
+    lib.lightning_attn_gated_recurrence_varlen.argtypes = [vp] * 7 + [i32] * 5 + [vp, sz, vp]
+    lib.lightning_attn_gated_recurrence_step.argtypes = [vp] * 4 + [i32] * 4 + [vp]
+    lib.lightning_attn_gated_recurrence_backward.argtypes = [vp] * 9 + [i32] * 5 + [vp, sz, vp]
+    lib.lightning_attn_gated_recurrence_backward_varlen.argtypes = [vp] * 10 + [i32] * 5 + [vp, sz, vp]
+    lib.lightning_attn_gated_recurrence_workspace_size.argtypes = [i32] * 5
+    lib.lightning_attn_gated_recurrence_workspace_size.restype = sz
+    lib.lightning_attn_layer_norm.argtypes = [vp] * 6 + [i32] * 3 + [f32, vp]
+    lib.lightning_attn_layer_norm_backward.argtypes = [vp] * 7 + [i32] * 3 + [f32, vp, sz, vp]
+    lib.lightning_attn_layer_norm_workspace_size.argtypes = [i32, i32]
+    lib.lightning_attn_layer_norm_workspace_size.restype = sz
     lib.lightning_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     lib.lightning_attn_workspace_size.restype = sz
     lib.lightning_attn_check.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint * 4)]
@@ -89,7 +111,10 @@ def _load():
               "lightning_attn_decode_step_znorm", "lightning_attn_decode_step",
               "lightning_attn_decode_step_noalloc", "lightning_attn_mixed_step", "lightning_attn_state_prefix", "lightning_attn_chunk_state",
               "lightning_attn_output_transform", "lightning_attn_output_transform_backward",
-              "lightning_attn_check"):
+              "lightning_attn_gated_recurrence", "lightning_attn_gated_recurrence_varlen",
+              "lightning_attn_gated_recurrence_step", "lightning_attn_gated_recurrence_backward",
+              "lightning_attn_gated_recurrence_backward_varlen", "lightning_attn_layer_norm",
+              "lightning_attn_layer_norm_backward", "lightning_attn_check"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -388,6 +413,173 @@ def lightning_attn_state_prefix(gathered, rank, out, state0=None, stream=None):
                                           _stream(stream))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_state_prefix")
+
+
+def _check_like(ref, *ts):
+    """Tensors of ref's shape and dtype, contiguous, all on the current CUDA device."""
+    if not ref.is_cuda:
+        raise ValueError(f"tensors must be on the current CUDA device, got {ref.device}")
+    dev = torch.cuda.current_device()
+    for t in (ref, *ts):
+        if t is None:
+            continue
+        if t.shape != ref.shape or t.dtype != ref.dtype:
+            raise ValueError(f"expected {ref.dtype} {tuple(ref.shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current CUDA device cuda:{dev}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return dev
+
+
+def _check_f32(dev, shape, *ts):
+    """fp32 tensors of `shape` (a tuple) on device `dev`, contiguous."""
+    for t in ts:
+        if t is not None:
+            _f32_or_none(t)
+            if t.shape != shape:
+                raise ValueError(f"expected float32 {tuple(shape)}, got {tuple(t.shape)}")
+            if t.get_device() != dev:
+                raise ValueError(f"tensors must be on the current CUDA device cuda:{dev}, got {t.device}")
+
+
+def _check_ws(dev, workspace):
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != dev or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
+    return 0 if workspace is None else workspace.numel()
+
+
+def _check_cu(dev, cu_seqlens):
+    _check_contig(cu_seqlens)
+    if cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be int32")
+    if cu_seqlens.dim() != 1 or cu_seqlens.get_device() != dev:
+        raise ValueError("cu_seqlens must be a 1-D tensor on the current CUDA device")
+    return cu_seqlens.numel() - 1
+
+
+def new_recurrence_checkpoints(tokens: int, W: int, device="cuda") -> torch.Tensor:
+    """The fp32 buffer a gated recurrence's forward over `tokens` packed rows (B * T) saves for
+    its backward."""
+    n = -(-int(tokens) // LA_RECURRENCE_CHECKPOINT_ROWS)
+    return torch.empty((n, int(W)), dtype=torch.float32, device=device)
+
+
+def lightning_attn_gated_recurrence_workspace_size(num_seqs: int, total_tokens: int, W: int, dtype: int,
+                                                   backward: bool = False) -> int:
+    return int(_lib.lightning_attn_gated_recurrence_workspace_size(num_seqs, total_tokens, W, dtype, int(backward)))
+
+
+def lightning_attn_gated_recurrence(x, f, out, state_in=None, state_out=None, checkpoints=None,
+                                    input_mode=LA_INPUT_TIED, workspace=None, stream=None):
+    """h_t = a_t h_{t-1} + b_t with a = sigmoid(f), b = x or (1 - a) x: x, f, out [B, T, W]; states
+    fp32 [B, W]; checkpoints from new_recurrence_checkpoints(B * T, W) (for the backward)."""
+    B, T, W = x.shape
+    dev = _check_like(x, f, out)
+    _check_f32(dev, (B, W), state_in, state_out)
+    _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
+    n = _check_ws(dev, workspace)
+    st = _lib.lightning_attn_gated_recurrence(_ptr(x), _ptr(f), _ptr(out), _ptr(state_in), _ptr(state_out),
+                                              _ptr(checkpoints), B, T, W, _dtype(x), input_mode, _ptr(workspace), n,
+                                              _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_gated_recurrence")
+
+
+def lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, state_in=None, state_out=None, checkpoints=None,
+                                           input_mode=LA_INPUT_TIED, workspace=None, stream=None):
+    """Packed sequences: x, f, out [total, W]; cu_seqlens int32 device [N + 1]; states fp32 [N, W]."""
+    total, W = x.shape
+    dev = _check_like(x, f, out)
+    n = _check_cu(dev, cu_seqlens)
+    _check_f32(dev, (n, W), state_in, state_out)
+    _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
+    nb = _check_ws(dev, workspace)
+    st = _lib.lightning_attn_gated_recurrence_varlen(_ptr(x), _ptr(f), _ptr(out), _ptr(state_in), _ptr(state_out),
+                                                     _ptr(checkpoints), _ptr(cu_seqlens), n, total, W, _dtype(x),
+                                                     input_mode, _ptr(workspace), nb, _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_gated_recurrence_varlen")
+
+
+def lightning_attn_gated_recurrence_step(x, f, out, state, input_mode=LA_INPUT_TIED, stream=None):
+    """One token per sequence: x, f, out [B, W]; state fp32 [B, W] updated in place."""
+    B, W = x.shape
+    dev = _check_like(x, f, out)
+    _check_f32(dev, (B, W), state)
+    st = _lib.lightning_attn_gated_recurrence_step(_ptr(x), _ptr(f), _ptr(out), _ptr(state), B, W, _dtype(x),
+                                                   input_mode, _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_gated_recurrence_step")
+
+
+def lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, state_in=None, dstate_out=None, dstate_in=None,
+                                             checkpoints=None, input_mode=LA_INPUT_TIED, workspace=None, stream=None):
+    """x, f, dout, dx, df [B, T, W]; states and their gradients fp32 [B, W]; checkpoints as the
+    forward wrote them, or None (recomputed)."""
+    B, T, W = x.shape
+    dev = _check_like(x, f, dout, dx, df)
+    _check_f32(dev, (B, W), state_in, dstate_out, dstate_in)
+    _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
+    n = _check_ws(dev, workspace)
+    st = _lib.lightning_attn_gated_recurrence_backward(_ptr(x), _ptr(f), _ptr(dout), _ptr(dx), _ptr(df),
+                                                       _ptr(state_in), _ptr(dstate_out), _ptr(dstate_in),
+                                                       _ptr(checkpoints), B, T, W, _dtype(x), input_mode,
+                                                       _ptr(workspace), n, _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_gated_recurrence_backward")
+
+
+def lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu_seqlens, state_in=None, dstate_out=None,
+                                                    dstate_in=None, checkpoints=None, input_mode=LA_INPUT_TIED,
+                                                    workspace=None, stream=None):
+    """x, f, dout, dx, df [total, W]; cu_seqlens int32 device [N + 1]; states and their gradients
+    fp32 [N, W]."""
+    total, W = x.shape
+    dev = _check_like(x, f, dout, dx, df)
+    n = _check_cu(dev, cu_seqlens)
+    _check_f32(dev, (n, W), state_in, dstate_out, dstate_in)
+    _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
+    nb = _check_ws(dev, workspace)
+    st = _lib.lightning_attn_gated_recurrence_backward_varlen(_ptr(x), _ptr(f), _ptr(dout), _ptr(dx), _ptr(df),
+                                                              _ptr(state_in), _ptr(dstate_out), _ptr(dstate_in),
+                                                              _ptr(checkpoints), _ptr(cu_seqlens), n, total, W,
+                                                              _dtype(x), input_mode, _ptr(workspace), nb,
+                                                              _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_gated_recurrence_backward_varlen")
+
+
+def lightning_attn_layer_norm_workspace_size(rows: int, W: int) -> int:
+    return int(_lib.lightning_attn_layer_norm_workspace_size(rows, W))
+
+
+def lightning_attn_layer_norm(x, out, residual=None, sum_out=None, weight=None, bias=None, eps=1e-5, stream=None):
+    """s = x + residual; out = (s - mean) / sqrt(var + eps) * weight + bias over the last axis:
+    x, residual, out, sum_out [..., W] (sum_out receives s); weight, bias fp32 [W] or None."""
+    W = x.shape[-1]
+    dev = _check_like(x, out, residual, sum_out)
+    _check_f32(dev, (W,), weight, bias)
+    st = _lib.lightning_attn_layer_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(out), _ptr(sum_out),
+                                        x.numel() // W if W else 0, W, _dtype(x), eps, _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_layer_norm")
+
+
+def lightning_attn_layer_norm_backward(s, dout, dx, dsum=None, weight=None, dweight=None, dbias=None, eps=1e-5,
+                                       workspace=None, stream=None):
+    """dx (and dweight, dbias fp32 [W]) from dout through the layer norm of s, plus dsum: s, dout,
+    dx, dsum [..., W]; s is the forward's sum_out (its x without a residual)."""
+    W = s.shape[-1]
+    dev = _check_like(s, dout, dx, dsum)
+    _check_f32(dev, (W,), weight, dweight, dbias)
+    n = _check_ws(dev, workspace)
+    st = _lib.lightning_attn_layer_norm_backward(_ptr(s), _ptr(dout), _ptr(dsum), _ptr(weight), _ptr(dx),
+                                                 _ptr(dweight), _ptr(dbias), s.numel() // W if W else 0, W, _dtype(s),
+                                                 eps, _ptr(workspace), n, _stream(stream))
+    if st != LA_OK:
+        raise LightningAttnError(st, "lightning_attn_layer_norm_backward")
 
 
 def lightning_attn_check(workspace, stream=None, raise_on_error=True):

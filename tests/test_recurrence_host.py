@@ -1,0 +1,336 @@
+"""The gated recurrence and the layer norm without a GPU: the fp64 references against finite
+differences and closed forms, the C entries' refusals, the binding's refusals, and the autograd
+functions' argument handling."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _recurrent_ref as ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_attn_b200 import build
+    return ctypes.CDLL(build.build())
+
+
+# --------------------------------------------------------------------------- references
+@pytest.mark.parametrize("tied", [False, True])
+def test_recurrence_gradient_against_differences(tied):
+    rng = np.random.default_rng(3)
+    T, W = 7, 3
+    x, f, dout = (rng.standard_normal((T, W)) for _ in range(3))
+    s0, ds1 = rng.standard_normal((2, W))
+    r = ref.sequence(x, f, tied, s0, dout, ds1)
+
+    def loss(x, f, s0):
+        q = ref.sequence(x, f, tied, s0)
+        return (q["out"] * dout).sum() + (q["state_out"] * ds1).sum()
+
+    step = 1e-6
+    for name, i in (("dx", 0), ("df", 1), ("dstate_in", 2)):
+        args = [x, f, s0]
+        d = rng.standard_normal(args[i].shape)
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + step * d, args[i] - step * d
+        slope = (loss(*up) - loss(*down)) / (2 * step)
+        assert abs(slope - (r[name] * d).sum()) <= 1e-7 * max(1.0, abs(slope)), name
+
+
+def test_recurrence_closed_forms():
+    T, W = 9, 2
+    x = np.arange(1.0, T * W + 1).reshape(T, W)
+    keepall = ref.sequence(x, np.full((T, W), np.inf), False)["out"]        # a = 1: running sums
+    np.testing.assert_allclose(keepall, np.cumsum(x, 0))
+    drop = ref.sequence(x, np.full((T, W), -np.inf), True)["out"]           # a = 0: the input itself
+    np.testing.assert_allclose(drop, x)
+    half = ref.sequence(np.ones((T, W)), np.zeros((T, W)), True)["out"]     # a = 1/2: 1 - 2^-t
+    np.testing.assert_allclose(half[:, 0], 1 - 0.5 ** np.arange(1, T + 1))
+
+
+def test_layer_norm_gradient_against_differences():
+    rng = np.random.default_rng(4)
+    s, dout, dsum = (rng.standard_normal((4, 6)) for _ in range(3))
+    w, b = rng.standard_normal((2, 6))
+    r = ref.layer_norm(s, w, b, 1e-5, dout, dsum)
+
+    def loss(s, w, b):
+        return (ref.layer_norm(s, w, b, 1e-5)["out"] * dout).sum() + (s * dsum).sum()
+
+    step = 1e-6
+    for name, i in (("dx", 0), ("dweight", 1), ("dbias", 2)):
+        args = [s, w, b]
+        d = rng.standard_normal(args[i].shape)
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + step * d, args[i] - step * d
+        slope = (loss(*up) - loss(*down)) / (2 * step)
+        assert abs(slope - (r[name] * d).sum()) <= 1e-7 * max(1.0, abs(slope)), name
+
+
+# --------------------------------------------------------------------------- C entries
+def _ptrs(n):
+    return [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(n)]
+
+
+ODD = ctypes.c_void_p(0x10008)
+WS = ctypes.c_void_p(0x1000000)
+
+
+def test_recurrence_entries_refuse(lib):
+    vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    fwd, var = lib.lightning_attn_gated_recurrence, lib.lightning_attn_gated_recurrence_varlen
+    bwd, bvar = lib.lightning_attn_gated_recurrence_backward, lib.lightning_attn_gated_recurrence_backward_varlen
+    step = lib.lightning_attn_gated_recurrence_step
+    fwd.argtypes = [vp] * 6 + [i32] * 5 + [vp, sz, vp]
+    var.argtypes = [vp] * 7 + [i32] * 5 + [vp, sz, vp]
+    bwd.argtypes = [vp] * 9 + [i32] * 5 + [vp, sz, vp]
+    bvar.argtypes = [vp] * 10 + [i32] * 5 + [vp, sz, vp]
+    step.argtypes = [vp] * 4 + [i32] * 4 + [vp]
+    p = _ptrs(12)
+
+    def call(fn, packed, backward, **kw):
+        a = dict(x=p[0], f=p[1], dout=p[2], out=p[3], df=p[4], s0=None, s1=None, ds1=None, ds0=None, ck=None, cu=p[5],
+                 n=2, T=8, W=64, dt=1, mode=1, ws=WS, nb=1 << 40)
+        a.update(kw)
+        state = [a["s0"], a["ds1"], a["ds0"]] if backward else [a["s0"], a["s1"]]
+        head = [a["x"], a["f"]] + ([a["dout"], a["out"], a["df"]] if backward else [a["out"]]) + state + [a["ck"]]
+        return fn(*head, *([a["cu"]] if packed else []), a["n"], a["T"], a["W"], a["dt"], a["mode"], a["ws"], a["nb"],
+                  None)
+
+    for fn, packed, backward in ((fwd, 0, 0), (var, 1, 0), (bwd, 0, 1), (bvar, 1, 1)):
+        bad = [dict(x=None), dict(f=None), dict(out=None), dict(x=ODD), dict(f=ODD), dict(out=ODD), dict(n=0),
+               dict(T=-1), dict(W=0), dict(dt=2), dict(mode=2), dict(mode=-1), dict(s0=ODD), dict(ck=ODD),
+               dict(ws=None), dict(ws=vp(0x1000010)), dict(nb=255), dict(out=p[0]), dict(out=p[1])]
+        if packed:
+            bad += [dict(cu=None), dict(cu=ODD)]
+        if backward:
+            bad += [dict(dout=None), dict(dout=ODD), dict(df=None), dict(df=ODD), dict(out=p[2]), dict(df=p[0]),
+                    dict(df=p[3]), dict(ds1=ODD), dict(ds0=ODD)]
+        else:
+            bad += [dict(s1=ODD)]
+        for kw in bad:
+            assert call(fn, packed, backward, **kw) == 1, (packed, backward, kw)
+    assert call(fwd, 0, 0, n=1 << 20, T=1 << 12) == 2       # 2^32 rows
+    assert call(bwd, 0, 1, n=1 << 20, T=1 << 12) == 2
+
+    for kw in (dict(x=None), dict(f=ODD), dict(out=p[0]), dict(out=p[1]), dict(st=None), dict(st=ODD), dict(B=0),
+               dict(W=0), dict(dt=5), dict(mode=3)):
+        a = dict(x=p[0], f=p[1], out=p[2], st=p[3], B=2, W=64, dt=1, mode=0)
+        a.update(kw)
+        assert step(a["x"], a["f"], a["out"], a["st"], a["B"], a["W"], a["dt"], a["mode"], None) == 1, kw
+
+
+def test_recurrence_workspace_size(lib):
+    f = lib.lightning_attn_gated_recurrence_workspace_size
+    f.restype = ctypes.c_size_t
+    for bad in ((0, 10, 8, 1, 0), (1, -1, 8, 1, 0), (1, 10, 0, 1, 0), (1, 10, 8, 2, 0)):
+        assert f(*bad) == 0, bad
+    small, back = f(2, 1000, 64, 1, 0), f(2, 1000, 64, 1, 1)
+    assert small >= 256 and back >= small + 8 * 64 * 4       # the backward's own checkpoints
+    assert f(1, 0, 64, 0, 0) >= 256
+
+
+def test_layer_norm_entries_refuse(lib):
+    vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    fwd, bwd = lib.lightning_attn_layer_norm, lib.lightning_attn_layer_norm_backward
+    fwd.argtypes = [vp] * 6 + [i32] * 3 + [f32, vp]
+    bwd.argtypes = [vp] * 7 + [i32] * 3 + [f32, vp, sz, vp]
+    p = _ptrs(8)
+
+    def f(**kw):
+        a = dict(x=p[0], res=None, w=None, b=None, out=p[1], sum=None, rows=4, W=64, dt=1, eps=1e-5)
+        a.update(kw)
+        return fwd(a["x"], a["res"], a["w"], a["b"], a["out"], a["sum"], a["rows"], a["W"], a["dt"], a["eps"], None)
+
+    def g(**kw):
+        a = dict(s=p[0], dout=p[1], dsum=None, w=None, dx=p[2], dw=p[3], db=p[4], rows=4, W=64, dt=1, eps=1e-5, ws=WS,
+                 nb=1 << 30)
+        a.update(kw)
+        return bwd(a["s"], a["dout"], a["dsum"], a["w"], a["dx"], a["dw"], a["db"], a["rows"], a["W"], a["dt"],
+                   a["eps"], a["ws"], a["nb"], None)
+
+    for kw in (dict(x=None), dict(out=None), dict(x=ODD), dict(out=ODD), dict(res=ODD), dict(w=ODD), dict(b=ODD),
+               dict(sum=ODD), dict(sum=p[1]), dict(rows=-1), dict(W=0), dict(dt=2), dict(eps=0.0),
+               dict(eps=float("nan"))):
+        assert f(**kw) == 1, kw
+    for kw in (dict(s=None), dict(dout=None), dict(dx=None), dict(s=ODD), dict(dout=ODD), dict(dx=ODD),
+               dict(dsum=ODD), dict(w=ODD), dict(dw=ODD), dict(db=ODD), dict(dw=p[4]), dict(rows=-1), dict(W=0),
+               dict(dt=2), dict(eps=0.0), dict(ws=None), dict(ws=vp(0x1000010)), dict(nb=16)):
+        assert g(**kw) == 1, kw
+    assert f(W=16385) == 2 and g(W=16385) == 2
+    assert f(rows=0, x=None, out=None) == 0                  # nothing to do
+    size = lib.lightning_attn_layer_norm_workspace_size
+    size.restype = ctypes.c_size_t
+    assert size(-1, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0
+    assert size(0, 64) >= 256 and size(100, 64) >= 2 * 64 * 4
+
+
+# --------------------------------------------------------------------------- binding
+def test_binding_refuses_host_tensors(lib):
+    from long_context_attn_b200 import lightning_attn as la
+    t = torch.zeros(2, 4, 8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        la.lightning_attn_gated_recurrence(t, t, t.clone())
+    with pytest.raises(ValueError, match="current CUDA device"):
+        la.lightning_attn_gated_recurrence_varlen(t[0], t[0], t[0].clone(), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        la.lightning_attn_gated_recurrence_step(t[0], t[0], t[0].clone(), torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        la.lightning_attn_layer_norm(t, t.clone())
+    with pytest.raises(ValueError, match="current CUDA device"):
+        la.lightning_attn_layer_norm_backward(t, t, t.clone())
+
+
+class _Recorder:
+    """Stands in for the binding: runs the fp64 references on CPU tensors."""
+    from long_context_attn_b200 import lightning_attn as _la
+    LA_INPUT_PLAIN, LA_INPUT_TIED = _la.LA_INPUT_PLAIN, _la.LA_INPUT_TIED
+
+    def __init__(self):
+        self.calls = []
+
+    def _dtype(self, t):
+        return 0
+
+    def new_workspace(self, n, device=None):
+        return torch.zeros(n, dtype=torch.uint8)
+
+    def new_recurrence_checkpoints(self, tokens, W, device=None):
+        return torch.zeros(-(-tokens // 128), W)
+
+    def lightning_attn_gated_recurrence_workspace_size(self, n, tokens, W, dtype, backward=False):
+        return 256
+
+    def lightning_attn_layer_norm_workspace_size(self, rows, W):
+        return 256
+
+    def _run(self, x, f, lens, mode, s0, dout=None, ds1=None):
+        n = lambda t: None if t is None else t.double().numpy()  # noqa: E731
+        W = x.shape[-1]
+        flat = lambda t: None if t is None else n(t).reshape(-1, W)  # noqa: E731
+        return ref.packed(flat(x), flat(f), lens, mode == self.LA_INPUT_TIED, n(s0), flat(dout), n(ds1))
+
+    def lightning_attn_gated_recurrence(self, x, f, out, s_in, s_out, saved, mode, ws):
+        self.calls.append("forward" if saved is not None else "forward without checkpoints")
+        r = self._run(x, f, [x.shape[1]] * x.shape[0], mode, s_in)
+        out.copy_(torch.from_numpy(r["out"]).view(x.shape))
+        s_out.copy_(torch.from_numpy(r["state_out"]))
+
+    def lightning_attn_gated_recurrence_varlen(self, x, f, out, cu, s_in, s_out, saved, mode, ws):
+        r = self._run(x, f, torch.diff(cu).tolist(), mode, s_in)
+        out.copy_(torch.from_numpy(r["out"]))
+        s_out.copy_(torch.from_numpy(r["state_out"]))
+
+    def _grads(self, r, x, dx, df, ds_in):
+        dx.copy_(torch.from_numpy(r["dx"]).view(x.shape))
+        df.copy_(torch.from_numpy(r["df"]).view(x.shape))
+        if ds_in is not None:
+            ds_in.copy_(torch.from_numpy(r["dstate_in"]))
+
+    def lightning_attn_gated_recurrence_backward(self, x, f, dout, dx, df, s_in, ds_out, ds_in, saved, mode, ws):
+        self._grads(self._run(x, f, [x.shape[1]] * x.shape[0], mode, s_in, dout, ds_out), x, dx, df, ds_in)
+
+    def lightning_attn_gated_recurrence_backward_varlen(self, x, f, dout, dx, df, cu, s_in, ds_out, ds_in, saved, mode,
+                                                        ws):
+        self._grads(self._run(x, f, torch.diff(cu).tolist(), mode, s_in, dout, ds_out), x, dx, df, ds_in)
+
+    def lightning_attn_layer_norm(self, x, out, residual=None, sum_out=None, weight=None, bias=None, eps=1e-5):
+        s = x if residual is None else x + residual
+        n = lambda t: None if t is None else t.double().numpy()  # noqa: E731
+        r = ref.layer_norm(n(s).reshape(-1, s.shape[-1]), n(weight), n(bias), eps)
+        out.copy_(torch.from_numpy(r["out"]).view(x.shape))
+        if sum_out is not None:
+            sum_out.copy_(s)
+
+    def lightning_attn_layer_norm_backward(self, s, dout, dx, dsum=None, weight=None, dweight=None, dbias=None,
+                                           eps=1e-5, workspace=None):
+        n = lambda t: None if t is None else t.double().numpy()  # noqa: E731
+        W = s.shape[-1]
+        r = ref.layer_norm(n(s).reshape(-1, W), n(weight), None, eps, n(dout).reshape(-1, W),
+                           None if dsum is None else n(dsum).reshape(-1, W))
+        dx.copy_(torch.from_numpy(r["dx"]).view(s.shape))
+        if dweight is not None:
+            dweight.copy_(torch.from_numpy(r["dweight"]))
+        if dbias is not None:
+            dbias.copy_(torch.from_numpy(r["dbias"]))
+
+
+@pytest.fixture
+def ag(monkeypatch):
+    from long_context_attn_b200 import autograd
+    fake = _Recorder()
+    monkeypatch.setattr(autograd, "la", fake)
+    autograd.fake = fake
+    return autograd
+
+
+def _leaf(rng, *shape):
+    return torch.tensor(rng.standard_normal(shape), dtype=torch.float32, requires_grad=True)
+
+
+def _plain_recurrence(x, f, lens, tied, s0):
+    a = torch.sigmoid(f)
+    b = (1 - a) * x if tied else x
+    outs, finals, at = [], [], 0
+    for i, m in enumerate(lens):
+        h = torch.zeros(x.shape[1], dtype=x.dtype) if s0 is None else s0[i]
+        for t in range(at, at + m):
+            h = a[t] * h + b[t]
+            outs.append(h)
+        finals.append(h)
+        at += m
+    return torch.stack(outs), torch.stack(finals)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("use", ["out", "state", "both"])
+def test_recurrence_autograd_wiring(ag, packed, use):
+    """Gradients through either output alone or both, against torch's own autograd."""
+    rng = np.random.default_rng(5)
+    lens = [4, 0, 1, 6] if packed else [5, 5]
+    W = 3
+    x, f, s0 = _leaf(rng, sum(lens), W), _leaf(rng, sum(lens), W), _leaf(rng, len(lens), W)
+    if packed:
+        cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32)
+        out, st = ag.gated_recurrence_varlen(x, f, cu, s0, input_mode=ag.fake.LA_INPUT_PLAIN)
+    else:
+        out, st = ag.gated_recurrence(x.view(2, 5, W), f.view(2, 5, W), s0, input_mode=ag.fake.LA_INPUT_PLAIN)
+    wo, ws = torch.randn(sum(lens), W), torch.randn(len(lens), W)
+    part = lambda o, s: {"out": (o.reshape(-1, W) * wo).sum(), "state": (s * ws).sum(),  # noqa: E731
+                         "both": (o.reshape(-1, W) * wo).sum() + (s * ws).sum()}[use]
+    got = torch.autograd.grad(part(out, st), (x, f, s0))
+    want = torch.autograd.grad(part(*_plain_recurrence(x, f, lens, False, s0)), (x, f, s0))
+    for g, w in zip(got, want):
+        torch.testing.assert_close(g, w, rtol=1e-4, atol=1e-5)
+
+
+def test_recurrence_without_gradients_saves_nothing(ag):
+    with torch.no_grad():
+        ag.gated_recurrence(torch.zeros(1, 4, 2), torch.zeros(1, 4, 2))
+    assert ag.fake.calls == ["forward without checkpoints"]
+
+
+@pytest.mark.parametrize("use", ["out", "sum", "both"])
+def test_layer_norm_autograd_wiring(ag, use):
+    rng = np.random.default_rng(6)
+    x, res, w, b = _leaf(rng, 2, 3, 6), _leaf(rng, 2, 3, 6), _leaf(rng, 6), _leaf(rng, 6)
+    out, s = ag.layer_norm(x, w, b, residual=res)
+    wo, ws = torch.randn(2, 3, 6), torch.randn(2, 3, 6)
+    part = lambda o, s: {"out": (o * wo).sum(), "sum": (s * ws).sum(), "both": (o * wo).sum() + (s * ws).sum()}[use]  # noqa: E731
+    got = torch.autograd.grad(part(out, s), (x, res, w, b), allow_unused=True)
+    want = torch.autograd.grad(part(torch.nn.functional.layer_norm(x + res, (6,), w, b, 1e-5), x + res),
+                               (x, res, w, b), allow_unused=True)
+    for g, v in zip(got, want):
+        torch.testing.assert_close(g, torch.zeros_like(g) if v is None else v, rtol=1e-4, atol=1e-5)
+
+
+def test_layer_norm_autograd_without_residual_or_weights(ag):
+    rng = np.random.default_rng(7)
+    x = _leaf(rng, 5, 6)
+    y = ag.layer_norm(x)
+    d = torch.randn(5, 6)
+    got, = torch.autograd.grad((y * d).sum(), x)
+    want, = torch.autograd.grad((torch.nn.functional.layer_norm(x, (6,)) * d).sum(), x)
+    torch.testing.assert_close(got, want, rtol=1e-4, atol=1e-5)
