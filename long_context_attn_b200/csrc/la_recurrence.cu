@@ -10,9 +10,10 @@
 // state_in instead, so packed sequences need no tiles of their own and cut the dependence.
 //
 // State entering a tile: tiles are handed out in time order by a ticket, so every tile before
-// one that runs has been started and never waits for a later one.  A warp looks back over the
-// tiles before its own until it finds one whose state after the last row is known, and folds the
-// (A, H) between from there, oldest first.  That fold does the same operations in the same
+// one that is worked on has been started and never waits for a later one.  A warp looks back over
+// the tiles before its own until it finds one whose state after the last row is known, and folds
+// the (A, H) between from there, oldest first.  Values and their being there are one word, read
+// and written whole, so the chain needs no flags and no fences.  That fold does the same operations in the same
 // order as the tiles' own (h <- A h + H, tile by tile), so the result does not depend on how
 // far the warp had to look.
 //
@@ -29,6 +30,22 @@ namespace {
 
 constexpr int kCkRows = LA_RECURRENCE_CHECKPOINT_ROWS;
 constexpr int kThreads = 256;
+#ifndef FB
+#define FB 2
+#endif
+#ifndef BB
+#define BB 2
+#endif
+#ifndef FSV
+#define FSV 8
+#define FSC 8
+#define FSR 4
+#endif
+#ifndef BSV
+#define BSV 4
+#define BSC 8
+#define BSR 4
+#endif
 
 struct RecArgs {
   const void *x, *f, *dout;
@@ -39,99 +56,194 @@ struct RecArgs {
   int nseq, T, W, tied;
   int64_t tokens;
   ErrRec* err;
-  // Chain between the tiles (more than one in time): cleared for each call.
+  // Chain between the tiles (more than one in time): all bits set before each walk.
   int ntiles, nblocks;          // in time, across the channels
-  unsigned int* ticket;         // [0]: next tile; [1]: a wait ran out, everybody gives up
-  unsigned int* flags;          // [ntiles][nblocks * C / 32]
-  float2* agg;                  // [ntiles][nblocks * C]: (A, H) of the tile
-  float* inc;                   // [ntiles][nblocks * C]: state after the tile
+  unsigned int* ticket;         // [0]: the last tile handed out; [1]: kOpen, until a wait ran out
+  uint64_t* agg;                // [ntiles][nblocks * C]: (A, H) of the tile
+  unsigned int* inc;            // [ntiles][nblocks * C]: state after the tile
 };
+// What a word of the chain holds until its value is there: a NaN that is never published.
+constexpr unsigned int kOpen = 0xFFFFFFFFu;
 
-// a = sigmoid(f) and 1 - a = sigmoid(-f), each without cancellation: with e = exp(-|f|) in
-// [0, 1], the larger of the two is 1 / (1 + e) and the smaller e / (1 + e).
-struct Gate {
-  float a, keep;
-};
-__device__ __forceinline__ Gate gate_of(float f) {
-  const float e = expf(-fabsf(f));
-  const float big = 1.0f / (1.0f + e), small = e * big;
-  return f >= 0.0f ? Gate{big, small} : Gate{small, big};
+// Two fp32 operations in one instruction (each rounded as the single one).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// a = sigmoid(f) = 1 / (1 + t) and keep = 1 - a = t / (1 + t) with t = exp(-f), neither by
+// cancellation.  Two special-function operations an element, exp2 and the reciprocal, which the
+// memory rate leaves room for.  bf16 gates take exp2 of the rounded product -f log2(e): t is
+// then off by at most (4 + |f|) 2^-24, against the 2^-9 the gate itself is rounded to (with expf
+// and an IEEE division the first tiled kernel spent 47 instructions an element and ran at 0.30
+// of the HBM rate, instruction-bound); fp32 gates call expf.  a is 0 where t leaves fp32's
+// normal range (f < -87.3), and keep, which t a would not give there, is 1.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T> __device__ __forceinline__ void gates(float2 f, float2& a, float2& keep) {
+  float2 t;
+  if constexpr (sizeof(T) == 2) {
+    const float2 y = mul2(f, splat(-1.4426950408889634f));
+    t = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+  } else {
+    t = make_float2(expf(-f.x), expf(-f.y));
+  }
+  const float2 d = add2(t, splat(1.0f));
+  a = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 k = mul2(t, a);
+  keep = make_float2(a.x == 0.0f ? 1.0f : k.x, a.y == 0.0f ? 1.0f : k.y);
 }
 
-// V consecutive channels of one row, as loaded.
+// V consecutive channels of one row, as loaded; they are worked on in pairs (V = 1: with an idle
+// second half).
 template <typename T, int V> struct Pack;
 template <> struct Pack<uint16_t, 8> {
   uint4 r;
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
-    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
-  __device__ __forceinline__ static Pack from(const float* o) {
-    return Pack{make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                           pack_bf16x2(o[6], o[7]))};
+  __device__ __forceinline__ static Pack from(const float2* o) {
+    return Pack{make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y), pack_bf16x2(o[2].x, o[2].y),
+                           pack_bf16x2(o[3].x, o[3].y))};
+  }
+};
+template <> struct Pack<uint16_t, 4> {
+  uint2 r;
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? r.x : r.y;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ static Pack from(const float2* o) {
+    return Pack{make_uint2(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y))};
   }
 };
 template <> struct Pack<float, 4> {
   float4 r;
-  __device__ __forceinline__ float get(int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
-  __device__ __forceinline__ static Pack from(const float* o) { return Pack{make_float4(o[0], o[1], o[2], o[3])}; }
+  __device__ __forceinline__ float2 pair(int i) const { return i == 0 ? make_float2(r.x, r.y) : make_float2(r.z, r.w); }
+  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{make_float4(o[0].x, o[0].y, o[1].x, o[1].y)}; }
 };
 template <> struct Pack<uint16_t, 1> {
   uint16_t r;
-  __device__ __forceinline__ float get(int) const { return bf16_bits_to_f32(r); }
-  __device__ __forceinline__ static Pack from(const float* o) { return Pack{f32_to_bf16_bits(o[0])}; }
+  __device__ __forceinline__ float2 pair(int) const { return make_float2(bf16_bits_to_f32(r), 0.f); }
+  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{f32_to_bf16_bits(o[0].x)}; }
 };
 template <> struct Pack<float, 1> {
   float r;
-  __device__ __forceinline__ float get(int) const { return r; }
-  __device__ __forceinline__ static Pack from(const float* o) { return Pack{o[0]}; }
+  __device__ __forceinline__ float2 pair(int) const { return make_float2(r, 0.f); }
+  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{o[0].x}; }
 };
-template <int V> __device__ __forceinline__ void load_f32(const float* p, float* o) {
+// V fp32 values of the states, the checkpoints or the folds.
+template <int V> __device__ __forceinline__ void load_f32(const float* p, float2* o) {
   if constexpr (V == 1) {
-    o[0] = *p;
+    o[0] = make_float2(*p, 0.f);
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
       const float4 t = *reinterpret_cast<const float4*>(p + i);
-      o[i] = t.x; o[i + 1] = t.y; o[i + 2] = t.z; o[i + 3] = t.w;
+      o[i / 2] = make_float2(t.x, t.y);
+      o[i / 2 + 1] = make_float2(t.z, t.w);
     }
   }
 }
-template <int V> __device__ __forceinline__ void store_f32(float* p, const float* o) {
+template <int V> __device__ __forceinline__ void store_f32(float* p, const float2* o) {
   if constexpr (V == 1) {
-    *p = o[0];
+    *p = o[0].x;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(o[i / 2].x, o[i / 2].y, o[i / 2 + 1].x, o[i / 2 + 1].y);
   }
 }
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 // CL threads side by side take V channels each; G = 256 / CL groups of them take R rows each.
 template <typename T_, int V_, int CL_, int R_> struct Shape {
   using T = T_;
-  static constexpr int V = V_, CL = CL_, R = R_;
+  static constexpr int V = V_, CL = CL_, R = R_, U = (V + 1) / 2;   // U pairs
   static constexpr int C = CL * V, G = kThreads / CL, L = G * R;
   static constexpr int NP = kThreads / C, GP = G / NP;   // the fold over groups: NP threads a channel
-  static_assert(C % 32 == 0 && kThreads % C == 0 && G % NP == 0 && kCkRows % R == 0, "tile");
+  static_assert(C % 32 == 0 && kThreads % C == 0 && G % NP == 0 && L == kCkRows, "tile");
 };
 
-template <class S> struct Smem {
+// A tile: its place in the walk and across the channels, whether a sequence starts or ends in its
+// rows (or they end), and the sequence of its first row (the first that ends behind it).
+struct Tile {
+  int k, cb, any, seq;
+};
+
+template <class S, int NT, int NB> struct Smem {
+  Pack<typename S::T, S::V> raw[NB][NT][S::R][kThreads];   // each thread's own, as the copies bring them
   float A[S::G][S::C], H[S::G][S::C];     // of each group; then H: the state entering it
   float pA[S::NP][S::C], pH[S::NP][S::C];
   float in[S::C];
-  int start[S::L], end[S::L];             // sequence that starts (ends) at the row, or -1
+  int start[2][S::L], end[2][S::L];       // of a tile with `any`: the sequence that starts (ends) at a row, or -1
   int reset[S::G], preset[S::NP];
-  int ticket;
+  Tile tile[3];
+};
+// The backward's: the same for the walk back (C, cin, creset) beside the walk forward in the tile.
+template <class S, int NT, int NB> struct SmemBack : Smem<S, NT, NB> {
+  float Cc[S::G][S::C], pC[S::NP][S::C], cin[S::C];
+  int creset[S::G], cpreset[S::NP];
 };
 
-__device__ __forceinline__ unsigned int load_acquire(const unsigned int* p) {
+// One vector into shared memory without waiting for it; zeros where `in` is false.
+template <typename P> __device__ __forceinline__ void copy_async(P* dst, const void* src, bool in) {
+  const unsigned int d = static_cast<unsigned int>(__cvta_generic_to_shared(dst));
+  if constexpr (sizeof(P) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else if constexpr (sizeof(P) == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(in ? 8 : 0) : "memory");
+  else
+    *dst = in ? *static_cast<const P*>(src) : P{};   // single elements: waited for
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ unsigned int load_relaxed(const unsigned int* p) {
   unsigned int v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_release(unsigned int* p, unsigned int v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ uint64_t load_relaxed(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
 }
+__device__ __forceinline__ void store_relaxed(unsigned int* p, unsigned int v) {
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_relaxed(uint64_t* p, uint64_t v) {
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+// The bits of a value of the chain: any NaN as the one that is not kOpen.
+__device__ __forceinline__ unsigned int published(float v) { return v == v ? __float_as_uint(v) : 0x7FC00000u; }
 
 // Rows of the packed batch that belong to a sequence: the first `limit` ones.
 __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
@@ -140,120 +252,175 @@ __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
   return n < 0 ? 0 : n < p.tokens ? n : p.tokens;
 }
 
-// Marks the rows of tile `j` where sequences start and end.  Ends with a barrier.
-template <int L> __device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int* start, int* end) {
-  const int tid = threadIdx.x;
+// Completes a tile (one thread).  Without `any`, every row of the tile is in one sequence and none
+// is its first or last.
+template <class S> __device__ __forceinline__ void look_up(const RecArgs& p, int64_t r0, int64_t limit, Tile& t) {
+  constexpr int L = S::L;
   if (!p.cu) {
-    for (int i = tid; i < L; i += kThreads) {
-      const int row = static_cast<int>(r0 + i);   // tokens <= INT32_MAX; rows behind them are marked in vain
-      const int s = row / p.T, t = row - s * p.T;
-      const bool in = r0 + i < p.tokens;
-      start[i] = in && t == 0 ? s : -1;
-      end[i] = in && t == p.T - 1 ? s : -1;
-    }
-    __syncthreads();
+    const unsigned int T = p.T, row = static_cast<unsigned int>(r0), s = row / T, in = row - s * T;
+    t.seq = static_cast<int>(s);
+    t.any = in == 0 || static_cast<int64_t>(in) + L >= T || r0 + L > limit;
     return;
   }
-  for (int i = tid; i < L; i += kThreads) start[i] = end[i] = -1;
-  __syncthreads();
-  int lo = 0, hi = p.nseq;   // first sequence whose rows end behind r0
+  int lo = 0, hi = p.nseq;
   while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (__ldg(p.cu + m + 1) > r0) hi = m; else lo = m + 1;
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid + 1) > r0) hi = mid; else lo = mid + 1;
   }
-  for (int s = lo + tid; s < p.nseq; s += kThreads) {
-    const int64_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
-    if (a >= r0 + L) break;
-    if (a < 0 || b <= a || b > p.tokens) continue;
-    if (a >= r0) start[a - r0] = s;
-    if (b - 1 >= r0 && b - 1 < r0 + L) end[b - 1 - r0] = s;
+  t.seq = lo;
+  t.any = lo >= p.nseq || __ldg(p.cu + lo) >= r0 || __ldg(p.cu + lo + 1) <= r0 + L || r0 + L > limit;
+}
+
+// Marks the rows of a tile with `any` where sequences start and end (a thread a row).
+template <class S>
+__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int seq, int* start, int* end) {
+  const int tid = threadIdx.x;
+  if (tid >= S::L) return;
+  const int64_t row = r0 + tid;
+  int st = -1, en = -1;
+  if (row < limit) {
+    if (!p.cu) {
+      const unsigned int T = p.T, s = static_cast<unsigned int>(row) / T, in = static_cast<unsigned int>(row) - s * T;
+      if (in == 0) st = static_cast<int>(s);
+      if (in == T - 1) en = static_cast<int>(s);
+    } else {
+      int a = seq, b = p.nseq;   // the sequence of this row
+      while (a < b) {
+        const int mid = (a + b) >> 1;
+        if (__ldg(p.cu + mid + 1) > row) b = mid; else a = mid + 1;
+      }
+      if (a < p.nseq) {
+        const int64_t first = __ldg(p.cu + a), last = static_cast<int64_t>(__ldg(p.cu + a + 1)) - 1;
+        if (first >= 0 && first <= row && last < p.tokens) {
+          if (first == row) st = a;
+          if (last == row) en = a;
+        }
+      }
+    }
   }
-  __syncthreads();
+  start[tid] = st;
+  end[tid] = en;
 }
 
 // Sequences without rows: their final state (gradient) is the initial (final) one.  Malformed
-// offsets are reported.  The sequences are dealt out to the time tiles.
-__device__ __forceinline__ void rowless_sequences(const RecArgs& p, int j, int c0, int cn, const float* from,
-                                                  float* to) {
+// offsets are reported.  A warp a sequence.
+__device__ __forceinline__ void rowless_sequences(const RecArgs& p, const float* from, float* to) {
   if (!p.cu) return;
-  for (int64_t s = static_cast<int64_t>(j) * kThreads + threadIdx.x; s < p.nseq;
-       s += static_cast<int64_t>(p.ntiles) * kThreads) {
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (kThreads / 32);
+  for (int64_t s = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); s < p.nseq; s += warps) {
     const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
     if (a < 0 || b < a || b > p.tokens || (s == 0 && a != 0)) {
-      report(p.err, LA_ERR_DEVICE, SITE_VARLEN_CU, static_cast<unsigned>(s), 0);
+      if (lane == 0) report(p.err, LA_ERR_DEVICE, SITE_VARLEN_CU, static_cast<unsigned>(s), 0);
     } else if (a == b && to) {
-      for (int c = c0; c < c0 + cn && c < p.W; ++c) to[s * p.W + c] = from ? from[s * p.W + c] : 0.f;
+      for (int c = lane; c < p.W; c += 32) to[s * p.W + c] = from ? from[s * p.W + c] : 0.f;
     }
   }
 }
 
-// One warp, 32 channels: what enters tile `k` (k counts tiles in the order of the walk; tile
-// -1 does not exist).  `sub`: the warp's column of flags; `c`: the lane's column of data.
-__device__ __forceinline__ float look_back(const RecArgs& p, int k, int sub, int nsub, int64_t c, int64_t cols) {
-  const int lane = threadIdx.x & 31;
-  int base = k - 1, from = -1;
-  const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns(p.err);
+// One warp, 32 channels, `col` the lane's: what enters the walk's tile k (> 0).
+__device__ __forceinline__ float look_back(const RecArgs& p, int k, int64_t col, int64_t cols) {
+  constexpr int K = 8;   // tiles looked at in one trip to L2
+  uint64_t t0 = 0;
+  int base = k - 1;
+  float h = 0.f;
   for (unsigned int polls = 0;;) {
-    const int i = base - lane;
-    const unsigned int st = i >= 0 ? load_acquire(p.flags + static_cast<int64_t>(i) * nsub + sub) : 2u;
-    const unsigned int known = __ballot_sync(0xffffffffu, st == 2u), open = __ballot_sync(0xffffffffu, st == 0u);
-    const unsigned int near = known ? (known & (0u - known)) - 1u : 0xffffffffu;   // tiles nearer than a known one
-    if ((open & near) == 0) {
-      if (known) {
-        from = base - (__ffs(known) - 1);
-        break;
-      }
-      base -= 32;   // 32 tiles whose (A, H) is there: look further back
-      continue;
+    unsigned int inc[K], known = 0, there = 0;
+    uint64_t agg[K];
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const int i = base - u < 0 ? 0 : base - u;
+      inc[u] = load_relaxed(p.inc + i * cols + col);
+      agg[u] = load_relaxed(p.agg + i * cols + col);
     }
-    if ((++polls & 63u) == 0) {
-      if (load_acquire(p.ticket + 1)) break;
-      if (globaltimer_ns() - t0 > limit) {
-        if (lane == 0) {
-          report(p.err, LA_ERR_TIMEOUT, SITE_RECURRENCE_CHAIN, static_cast<unsigned>(k), static_cast<unsigned>(sub));
-          store_release(p.ticket + 1, 1u);
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      known |= static_cast<unsigned int>(inc[u] != kOpen) << u;
+      there |= static_cast<unsigned int>(static_cast<unsigned int>(agg[u]) != kOpen) << u;
+    }
+    known = __reduce_and_sync(0xffffffffu, known);
+    there = __reduce_and_sync(0xffffffffu, there);
+    const unsigned int near = known ? (known & (0u - known)) - 1u : (1u << K) - 1u;   // tiles nearer than a known one
+    if ((there & near) == near) {
+      if (!known) {
+        base -= K;   // all (A, H) there: look further back
+        continue;
+      }
+      // the known state, then the tiles of this window behind it, oldest first
+#pragma unroll
+      for (int u = K - 1; u >= 0; --u) {
+        if (near >> u & 1u)
+          h = fmaf(__uint_as_float(static_cast<unsigned int>(agg[u])), h,
+                   __uint_as_float(static_cast<unsigned int>(agg[u] >> 32)));
+        else if (known >> u & 1u)
+          h = __uint_as_float(inc[u]);
+      }
+      break;
+    }
+    if ((++polls & 63u) == 0) {   // no progress: has somebody given up, or is it time to?
+      if (load_relaxed(p.ticket + 1) != kOpen) return 0.f;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > wait_limit_ns(p.err)) {
+        if ((threadIdx.x & 31) == 0) {
+          report(p.err, LA_ERR_TIMEOUT, SITE_RECURRENCE_CHAIN, static_cast<unsigned>(k), static_cast<unsigned>(col));
+          store_relaxed(p.ticket + 1, 0u);
         }
-        break;
+        return 0.f;
       }
     }
   }
-  __syncwarp();
-  if (from < 0) return 0.f;
-  float h = __ldcg(p.inc + from * cols + c);
-  int i = from + 1;
-  for (; i + 8 <= k; i += 8) {
-    float2 t[8];
+  for (int i = base + 1; i < k; i += K) {   // the windows passed on the way
+    uint64_t t[K];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) t[u] = __ldcg(p.agg + (i + u) * cols + c);
+    for (int u = 0; u < K; ++u) t[u] = load_relaxed(p.agg + (i + u) * cols + col);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) h = fmaf(t[u].x, h, t[u].y);
-  }
-  for (; i < k; ++i) {
-    const float2 t = __ldcg(p.agg + i * cols + c);
-    h = fmaf(t.x, h, t.y);
+    for (int u = 0; u < K; ++u)
+      h = fmaf(__uint_as_float(static_cast<unsigned int>(t[u])), h, __uint_as_float(static_cast<unsigned int>(t[u] >> 32)));
   }
   return h;
 }
 
-// The fold over the CTA's groups and, through the chain, over the tiles before it: on return
-// sm.H[g] is what enters group g.  On entry sm.A, sm.H, sm.reset hold each group's (A, H) and
-// whether a sequence starts in it, so that what enters it does not leave it (and is not
-// multiplied: it may be infinite).  Nothing (0) enters the walk's first tile.
-// BACK: groups and tiles are walked from the last to the first.
-template <class S, bool BACK>
-__device__ __forceinline__ void fold_groups(const RecArgs& p, Smem<S>& sm, int k, int cb) {
-  constexpr int C = S::C, NP = S::NP, GP = S::GP, G = S::G;
+// What the chain knows of the walk's tile k is (tA, tH), with `cut` set where a sequence starts
+// in it, so that what enters it does not leave it: published; returns what enters the tile.
+// `meanwhile` runs before the wait.  One warp, 32 channels, `col` the lane's.
+template <class F>
+__device__ __forceinline__ float chain(const RecArgs& p, int k, int64_t col, int64_t cols, float tA, float tH, int cut,
+                                       F meanwhile) {
+  if (p.ntiles == 1) {
+    meanwhile();
+    return 0.f;
+  }
+  if (cut || k == 0)
+    store_relaxed(p.inc + k * cols + col, published(tH));
+  else
+    store_relaxed(p.agg + k * cols + col, static_cast<uint64_t>(published(tH)) << 32 | published(tA));
+  meanwhile();
+  if (k == 0) return 0.f;   // nothing enters the first tile
+  const float in = look_back(p, k, col, cols);
+  if (!cut) store_relaxed(p.inc + k * cols + col, published(fmaf(tA, in, tH)));
+  return in;
+}
+
+// Acts on h as a run of rows with (A, H) does; `cut`: what enters the run does not leave it (and
+// is not multiplied by 0: it may be infinite).
+__device__ __forceinline__ float act(int cut, float A, float H, float h) { return cut ? H : fmaf(A, h, H); }
+
+// The fold over the CTA's groups and, through the chain, over the tiles before it.  On entry sm.A,
+// sm.H, sm.reset hold each group's (A, H) and whether a sequence starts in it; on return sm.H[g]
+// is what enters group g.  `meanwhile` runs once in every thread, before the wait.
+template <class S, class M, class F>
+__device__ __forceinline__ void fold_forward(const RecArgs& p, M& sm, int k, int cb, F meanwhile) {
+  constexpr int C = S::C, NP = S::NP, GP = S::GP;
   const int c = threadIdx.x % C, part = threadIdx.x / C;
   float A[GP], H[GP];
   float pa = 1.f, ph = 0.f;
   int pr = 0;
 #pragma unroll
   for (int i = 0; i < GP; ++i) {
-    const int g = BACK ? G - 1 - (part * GP + i) : part * GP + i;
+    const int g = part * GP + i, r = sm.reset[g];
     A[i] = sm.A[g][c];
     H[i] = sm.H[g][c];
-    const int r = sm.reset[g];
-    ph = r ? H[i] : fmaf(A[i], ph, H[i]);
+    ph = act(r, A[i], H[i], ph);
     pa *= A[i];
     pr |= r;
   }
@@ -262,262 +429,435 @@ __device__ __forceinline__ void fold_groups(const RecArgs& p, Smem<S>& sm, int k
   if (c == 0) sm.preset[part] = pr;
   __syncthreads();
   if (part == 0) {   // whole warps: C is a multiple of 32
-    const int64_t cols = static_cast<int64_t>(p.nblocks) * C, col = static_cast<int64_t>(cb) * C + c;
-    const int nsub = static_cast<int>(cols / 32), sub = static_cast<int>(col / 32);
-    const bool chain = p.ntiles > 1;
     float tA = 1.f, tH = 0.f;
-    int tr = 0;
+    int cut = 0;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      tH = sm.preset[i] ? sm.pH[i][c] : fmaf(sm.pA[i][c], tH, sm.pH[i][c]);
+      tH = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], tH);
       tA *= sm.pA[i][c];
-      tr |= sm.preset[i];
+      cut |= sm.preset[i];
     }
-    unsigned int* flag = p.flags + static_cast<int64_t>(k) * nsub + sub;
-    const bool alone = tr || k == 0;   // what leaves the tile does not need the tiles before it
-    float in = 0.f;
-    if (chain) {
-      if (alone) p.inc[k * cols + col] = tH;
-      else p.agg[k * cols + col] = make_float2(tA, tH);
-      __syncwarp();
-      if ((c & 31) == 0) store_release(flag, alone ? 2u : 1u);
-      if (k > 0) {
-        in = look_back(p, k, sub, nsub, col, cols);
-        if (!alone) {
-          p.inc[k * cols + col] = fmaf(tA, in, tH);
-          __syncwarp();
-          if ((c & 31) == 0) store_release(flag, 2u);
-        }
-      }
-    }
-    sm.in[c] = in;
+    sm.in[c] = chain(p, k, static_cast<int64_t>(cb) * C + c, static_cast<int64_t>(p.nblocks) * C, tA, tH, cut, meanwhile);
+  } else {
+    meanwhile();
   }
   __syncthreads();
   float h = sm.in[c];
 #pragma unroll
   for (int i = 0; i < NP; ++i)
-    if (i < part) h = sm.preset[i] ? sm.pH[i][c] : fmaf(sm.pA[i][c], h, sm.pH[i][c]);
+    if (i < part) h = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], h);
 #pragma unroll
   for (int i = 0; i < GP; ++i) {
-    const int g = BACK ? G - 1 - (part * GP + i) : part * GP + i;
+    const int g = part * GP + i;
     sm.H[g][c] = h;
-    h = sm.reset[g] ? H[i] : fmaf(A[i], h, H[i]);
+    h = act(sm.reset[g], A[i], H[i], h);
   }
   __syncthreads();
 }
 
-template <class S, bool TIED> __global__ void __launch_bounds__(kThreads) rec_forward_kernel(RecArgs p) {
-  using T = typename S::T;
-  constexpr int V = S::V, R = S::R;
-  __shared__ Smem<S> sm;
-  const int tid = threadIdx.x, cl = tid % S::CL, g = tid / S::CL;
-  if (tid == 0) sm.ticket = p.ntiles > 1 ? static_cast<int>(atomicAdd(p.ticket, 1u)) : static_cast<int>(blockIdx.x);
+// The backward's folds, both at once: forward in the tile from the checkpoint `ck` (the thread's
+// channel's), and from the last group to the first, through the chain, of what flows back:
+// on return sm.H[g] and sm.Cc[g] are what enters group g from before and from behind.
+template <class S, class M, class F>
+__device__ __forceinline__ void fold_both(const RecArgs& p, M& sm, int k, int cb, float ck, F meanwhile) {
+  constexpr int C = S::C, NP = S::NP, GP = S::GP;
+  const int c = threadIdx.x % C, part = threadIdx.x / C;
+  float A[GP], H[GP], Cc[GP];
+  float pa = 1.f, ph = 0.f, pc = 0.f;
+  int pr = 0, pe = 0;
+#pragma unroll
+  for (int i = 0; i < GP; ++i) {
+    const int g = part * GP + i, r = sm.reset[g];
+    A[i] = sm.A[g][c];
+    H[i] = sm.H[g][c];
+    Cc[i] = sm.Cc[g][c];
+    ph = act(r, A[i], H[i], ph);
+    pa *= A[i];
+    pr |= r;
+  }
+#pragma unroll
+  for (int i = GP - 1; i >= 0; --i) {
+    const int e = sm.creset[part * GP + i];
+    pc = act(e, A[i], Cc[i], pc);
+    pe |= e;
+  }
+  sm.pA[part][c] = pa;
+  sm.pH[part][c] = ph;
+  sm.pC[part][c] = pc;
+  if (c == 0) {
+    sm.preset[part] = pr;
+    sm.cpreset[part] = pe;
+  }
   __syncthreads();
-  const int k = sm.ticket / p.nblocks, cb = sm.ticket % p.nblocks;
-  const int64_t r0 = static_cast<int64_t>(k) * S::L, row0 = r0 + g * R;
-  const int c0 = cb * S::C + cl * V;
-  const bool in = c0 < p.W;
-  const T* x = static_cast<const T*>(p.x) + row0 * p.W + c0;
-  const T* f = static_cast<const T*>(p.f) + row0 * p.W + c0;
-  Pack<T, V> xr[R], fr[R];
+  if (part == 0) {
+    float tA = 1.f, tC = 0.f;
+    int cut = 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (in && row0 + i < p.tokens) {
-      xr[i] = *reinterpret_cast<const Pack<T, V>*>(x + static_cast<int64_t>(i) * p.W);
-      fr[i] = *reinterpret_cast<const Pack<T, V>*>(f + static_cast<int64_t>(i) * p.W);
-    } else {
-      xr[i] = fr[i] = Pack<T, V>{};
+    for (int i = NP - 1; i >= 0; --i) {
+      tC = act(sm.cpreset[i], sm.pA[i][c], sm.pC[i][c], tC);
+      tA *= sm.pA[i][c];
+      cut |= sm.cpreset[i];
     }
+    sm.cin[c] = chain(p, k, static_cast<int64_t>(cb) * C + c, static_cast<int64_t>(p.nblocks) * C, tA, tC, cut, meanwhile);
+  } else {
+    meanwhile();
   }
-  const int64_t limit = row_limit(p);
-  rowless_sequences(p, k, cb * S::C, S::C, p.s0, p.s1);
-  if (r0 >= limit) return;   // no later tile has rows either
-  mark_rows<S::L>(p, r0, sm.start, sm.end);
-
-  float a[R][V], b[R][V], A[V], H[V];
-  int reset = 0;
+  float h = ck;
 #pragma unroll
-  for (int e = 0; e < V; ++e) { A[e] = 1.f; H[e] = 0.f; }
+  for (int i = 0; i < NP; ++i)
+    if (i < part) h = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], h);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int s = sm.start[g * R + i];
-    if (s >= 0) {
-      reset = 1;
-#pragma unroll
-      for (int e = 0; e < V; ++e) H[e] = 0.f;
-      if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const Gate q = gate_of(fr[i].get(e));
-      const float xv = xr[i].get(e);
-      a[i][e] = q.a;
-      b[i][e] = TIED ? q.keep * xv : xv;
-      H[e] = fmaf(a[i][e], H[e], b[i][e]);
-      A[e] *= a[i][e];
-    }
+  for (int i = 0; i < GP; ++i) {
+    const int g = part * GP + i;
+    sm.H[g][c] = h;
+    h = act(sm.reset[g], A[i], H[i], h);
   }
-  store_f32<V>(&sm.A[g][cl * V], A);
-  store_f32<V>(&sm.H[g][cl * V], H);
-  if (cl == 0) sm.reset[g] = reset;
   __syncthreads();
-  fold_groups<S, false>(p, sm, k, cb);
-
-  if (!in) return;
-  float h[V];
-  load_f32<V>(&sm.H[g][cl * V], h);
-  T* out = p.out ? static_cast<T*>(p.out) + row0 * p.W + c0 : nullptr;
+  float b = sm.cin[c];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (row0 + i >= limit) break;
-    const int s = sm.start[g * R + i], e1 = sm.end[g * R + i];
-    if (s >= 0) {
+  for (int i = NP - 1; i >= 0; --i)
+    if (i > part) b = act(sm.cpreset[i], sm.pA[i][c], sm.pC[i][c], b);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = 0.f;
-      if (p.s0) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
-    }
-    if (p.ck && (row0 + i) % kCkRows == 0) store_f32<V>(p.ck + (row0 + i) / kCkRows * p.W + c0, h);
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = fmaf(a[i][e], h[e], b[i][e]);
-    if (out) *reinterpret_cast<Pack<T, V>*>(out + static_cast<int64_t>(i) * p.W) = Pack<T, V>::from(h);
-    if (e1 >= 0 && p.s1) store_f32<V>(p.s1 + static_cast<int64_t>(e1) * p.W + c0, h);
+  for (int i = GP - 1; i >= 0; --i) {
+    const int g = part * GP + i;
+    sm.Cc[g][c] = b;
+    b = act(sm.creset[g], A[i], Cc[i], b);
   }
+  __syncthreads();
 }
 
-template <class S, bool TIED> __global__ void __launch_bounds__(kThreads) rec_backward_kernel(RecArgs p) {
+// The tiles a CTA works on, one after the other: by ticket where tiles wait for one another, so
+// that a tile is only waited for once somebody works on it (tickets are drawn ahead, but in
+// order: the holder of the smallest unfinished one works on it), else dealt out.
+__device__ __forceinline__ int next_tile(const RecArgs& p, int nth) {
+  if (p.ntiles > 1) return static_cast<int>(atomicAdd(p.ticket, 1u) + 1u);
+  return static_cast<int>(blockIdx.x + static_cast<unsigned int>(nth) * gridDim.x);
+}
+__device__ __forceinline__ void place(const RecArgs& p, int tile, Tile& t) {
+  t.k = tile / p.nblocks;
+  t.cb = tile - t.k * p.nblocks;
+}
+
+// Both walks.  Ahead of the tile being worked on, the next one's rows are on their way into shared
+// memory and the one's after it are asked for; `scout`, a thread of the last warp, draws and looks
+// up the tiles while the first warps wait for the chain.
+template <class S, bool TIED> __global__ void __launch_bounds__(kThreads, FB) rec_forward_kernel(RecArgs p) {
   using T = typename S::T;
-  constexpr int V = S::V, R = S::R, G = S::G;
-  static_assert(S::L == kCkRows, "a tile starts at a checkpoint");
-  __shared__ Smem<S> sm;
+  using P = Pack<T, S::V>;
+  constexpr int V = S::V, R = S::R, U = S::U;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  auto& sm = *reinterpret_cast<Smem<S, 2, 2>*>(smem_raw);
   const int tid = threadIdx.x, cl = tid % S::CL, g = tid / S::CL;
-  if (tid == 0) sm.ticket = p.ntiles > 1 ? static_cast<int>(atomicAdd(p.ticket, 1u)) : static_cast<int>(blockIdx.x);
-  __syncthreads();
-  const int k = sm.ticket / p.nblocks, cb = sm.ticket % p.nblocks;
-  const int j = p.ntiles - 1 - k;   // the walk goes backwards in time
-  const int64_t r0 = static_cast<int64_t>(j) * S::L, row0 = r0 + g * R;
-  const int c0 = cb * S::C + cl * V;
-  const bool in = c0 < p.W;
-  const int64_t at = row0 * p.W + c0;
-  Pack<T, V> xr[R], fr[R], dr[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t o = at + static_cast<int64_t>(i) * p.W;
-    if (in && row0 + i < p.tokens) {
-      xr[i] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.x) + o);
-      fr[i] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.f) + o);
-      dr[i] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.dout) + o);
-    } else {
-      xr[i] = fr[i] = dr[i] = Pack<T, V>{};
-    }
-  }
+  const bool scout = tid == kThreads - 32;
   const int64_t limit = row_limit(p);
-  rowless_sequences(p, j, cb * S::C, S::C, p.ds1, p.ds0);
-  mark_rows<S::L>(p, r0, sm.start, sm.end);
+  const int filled = static_cast<int>((limit + S::L - 1) / S::L);   // tiles with rows, in time
+  rowless_sequences(p, p.s0, p.s1);
 
-  // Forward in time inside the tile: the state entering each group.
-  float a[R][V], A[V], H[V];
-  int reset = 0;
+  auto fetch = [&](const Tile& t, int buf) {   // a group for every call, so that they can be counted
+    if (t.k < filled) {
+      const int64_t row0 = static_cast<int64_t>(t.k) * S::L + g * R;
+      const int c0 = t.cb * S::C + cl * V;
+      const T* x = static_cast<const T*>(p.x) + row0 * p.W + c0;
+      const T* f = static_cast<const T*>(p.f) + row0 * p.W + c0;
+      if (c0 < p.W && row0 + R <= limit) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) { A[e] = 1.f; H[e] = 0.f; }
+        for (int i = 0; i < R; ++i, x += p.W, f += p.W) {
+          copy_async(&sm.raw[buf][0][i][tid], x, true);
+          copy_async(&sm.raw[buf][1][i][tid], f, true);
+        }
+      } else {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int s = sm.start[g * R + i];
-    if (s >= 0) {
-      reset = 1;
-#pragma unroll
-      for (int e = 0; e < V; ++e) H[e] = 0.f;
-      if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
+        for (int i = 0; i < R; ++i, x += p.W, f += p.W) {
+          const bool in = c0 < p.W && row0 + i < limit;
+          copy_async(&sm.raw[buf][0][i][tid], in ? x : static_cast<const T*>(p.x), in);
+          copy_async(&sm.raw[buf][1][i][tid], in ? f : static_cast<const T*>(p.f), in);
+        }
+      }
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const Gate q = gate_of(fr[i].get(e));
-      const float xv = xr[i].get(e);
-      a[i][e] = q.a;
-      H[e] = fmaf(q.a, H[e], TIED ? q.keep * xv : xv);
-      A[e] *= q.a;
-    }
-  }
-  store_f32<V>(&sm.A[g][cl * V], A);
-  store_f32<V>(&sm.H[g][cl * V], H);
-  if (cl == 0) sm.reset[g] = reset;
-  __syncthreads();
-  if (tid < S::C) {   // one thread a channel, group by group
-    const int c = cb * S::C + tid;
-    float h = r0 < limit && c < p.W ? p.ck[static_cast<int64_t>(j) * p.W + c] : 0.f;
-#pragma unroll 4
-    for (int i = 0; i < G; ++i) {
-      const float hi = sm.H[i][tid];
-      sm.H[i][tid] = h;
-      h = sm.reset[i] ? hi : fmaf(sm.A[i][tid], h, hi);
+    copy_commit();
+  };
+  if (scout) {
+    for (int n = 0; n < 2; ++n) {
+      place(p, next_tile(p, n), sm.tile[n]);
+      if (sm.tile[n].k < filled) look_up<S>(p, static_cast<int64_t>(sm.tile[n].k) * S::L, limit, sm.tile[n]);
     }
   }
   __syncthreads();
-  float prev[R][V], h[V];
-  load_f32<V>(&sm.H[g][cl * V], h);
-  // Backward in time: what each group adds to the flow into the state before it.
-  float cc[V];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int s = sm.start[g * R + i];
-    if (s >= 0) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = 0.f;
-      if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      prev[i][e] = h[e];
-      const float xv = xr[i].get(e);
-      h[e] = fmaf(a[i][e], h[e], TIED ? gate_of(fr[i].get(e)).keep * xv : xv);
-    }
-  }
-  reset = 0;
-#pragma unroll
-  for (int e = 0; e < V; ++e) cc[e] = 0.f;
-#pragma unroll
-  for (int i = R - 1; i >= 0; --i) {
-    const int s = sm.end[g * R + i];
-    if (s >= 0) {
-      reset = 1;
-#pragma unroll
-      for (int e = 0; e < V; ++e) cc[e] = 0.f;
-      if (p.ds1 && in) load_f32<V>(p.ds1 + static_cast<int64_t>(s) * p.W + c0, cc);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) cc[e] = a[i][e] * (dr[i].get(e) + cc[e]);
-  }
+  Tile tile = sm.tile[0];
+  fetch(tile, 0);
+  fetch(sm.tile[1], 1);
+  if (tile.k < filled && tile.any)
+    mark_rows<S>(p, static_cast<int64_t>(tile.k) * S::L, limit, tile.seq, sm.start[0], sm.end[0]);
   __syncthreads();
-  store_f32<V>(&sm.H[g][cl * V], cc);
-  if (cl == 0) sm.reset[g] = reset;
-  __syncthreads();
-  fold_groups<S, true>(p, sm, k, cb);
+  int slot = 0;   // n % 3
+  for (int n = 0; tile.k < filled; ++n) {
+    const int buf = n & 1, slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+    const int64_t row0 = static_cast<int64_t>(tile.k) * S::L + g * R;
+    const int c0 = tile.cb * S::C + cl * V;
+    const bool in = c0 < p.W;
+    int drawn = 0;
+    if (scout) drawn = next_tile(p, n + 2);
+    copy_wait<1>();
 
-  if (!in) return;
-  load_f32<V>(&sm.H[g][cl * V], cc);
+    float2 a[R][U], b[R][U], A[U], H[U];
+    int reset = 0;
 #pragma unroll
-  for (int i = R - 1; i >= 0; --i) {
-    if (row0 + i >= limit) continue;
-    const int s = sm.start[g * R + i], e1 = sm.end[g * R + i];
-    if (e1 >= 0) {
+    for (int e = 0; e < U; ++e) { A[e] = splat(1.f); H[e] = splat(0.f); }
+    auto rows_in = [&](auto marked) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) cc[e] = 0.f;
-      if (p.ds1) load_f32<V>(p.ds1 + static_cast<int64_t>(e1) * p.W + c0, cc);
+      for (int i = 0; i < R; ++i) {
+        const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
+        if constexpr (decltype(marked)::value) {
+          const int s = sm.start[buf][g * R + i];
+          if (s >= 0) {
+            reset = 1;
+#pragma unroll
+            for (int e = 0; e < U; ++e) H[e] = splat(0.f);
+            if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          float2 keep;
+          gates<T>(fr.pair(e), a[i][e], keep);
+          b[i][e] = TIED ? mul2(keep, xr.pair(e)) : xr.pair(e);
+          H[e] = fma2(a[i][e], H[e], b[i][e]);
+          A[e] = mul2(A[e], a[i][e]);
+        }
+      }
+    };
+    if (tile.any) rows_in(Yes{}); else rows_in(No{});
+    store_f32<V>(&sm.A[g][cl * V], A);
+    store_f32<V>(&sm.H[g][cl * V], H);
+    if (cl == 0) sm.reset[g] = reset;
+    if (scout) place(p, drawn, sm.tile[slot2]);
+    __syncthreads();
+    const Tile next = sm.tile[slot1];
+    fold_forward<S>(p, sm, tile.k, tile.cb, [&] {
+      fetch(sm.tile[slot2], buf);
+      if (next.k < filled && next.any)
+        mark_rows<S>(p, static_cast<int64_t>(next.k) * S::L, limit, next.seq, sm.start[buf ^ 1], sm.end[buf ^ 1]);
+      if (scout && sm.tile[slot2].k < filled)
+        look_up<S>(p, static_cast<int64_t>(sm.tile[slot2].k) * S::L, limit, sm.tile[slot2]);
+    });
+
+    if (in) {
+      float2 h[U];
+      load_f32<V>(&sm.H[g][cl * V], h);
+      T* out = p.out ? static_cast<T*>(p.out) + row0 * p.W + c0 : nullptr;
+      auto rows_out = [&](auto marked) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if constexpr (decltype(marked)::value) {
+            if (row0 + i >= limit) break;
+            const int s = sm.start[buf][g * R + i];
+            if (s >= 0) {
+#pragma unroll
+              for (int e = 0; e < U; ++e) h[e] = splat(0.f);
+              if (p.s0) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
+            }
+          }
+          if (i == 0 && g == 0 && p.ck) store_f32<V>(p.ck + static_cast<int64_t>(tile.k) * p.W + c0, h);
+#pragma unroll
+          for (int e = 0; e < U; ++e) h[e] = fma2(a[i][e], h[e], b[i][e]);
+          if (out) {
+            *reinterpret_cast<P*>(out) = P::from(h);
+            out += p.W;
+          }
+          if constexpr (decltype(marked)::value) {
+            const int s = sm.end[buf][g * R + i];
+            if (s >= 0 && p.s1) store_f32<V>(p.s1 + static_cast<int64_t>(s) * p.W + c0, h);
+          }
+        }
+      };
+      if (tile.any) rows_out(Yes{}); else rows_out(No{});
     }
-    float dx[V], df[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float keep = gate_of(fr[i].get(e)).keep;
-      const float G1 = dr[i].get(e) + cc[e];
-      const float kg = keep * G1;
-      dx[e] = TIED ? kg : G1;
-      df[e] = kg * a[i][e] * (TIED ? prev[i][e] - xr[i].get(e) : prev[i][e]);
-      cc[e] = a[i][e] * G1;
-    }
-    const int64_t o = at + static_cast<int64_t>(i) * p.W;
-    *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.dx) + o) = Pack<T, V>::from(dx);
-    *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.df) + o) = Pack<T, V>::from(df);
-    if (s >= 0 && p.ds0) store_f32<V>(p.ds0 + static_cast<int64_t>(s) * p.W + c0, cc);
+    tile = next;
+    slot = slot1;
   }
+  copy_wait<0>();
+}
+
+template <class S, bool TIED> __global__ void __launch_bounds__(kThreads, BB) rec_backward_kernel(RecArgs p) {
+  using T = typename S::T;
+  using P = Pack<T, S::V>;
+  constexpr int V = S::V, R = S::R, U = S::U;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  auto& sm = *reinterpret_cast<SmemBack<S, 3, 2>*>(smem_raw);
+  const int tid = threadIdx.x, cl = tid % S::CL, g = tid / S::CL;
+  const bool scout = tid == kThreads - 32;
+  const int64_t limit = row_limit(p);
+  const int filled = static_cast<int>((limit + S::L - 1) / S::L);
+  rowless_sequences(p, p.ds1, p.ds0);
+
+  auto first_row = [&](const Tile& t) { return static_cast<int64_t>(filled - 1 - t.k) * S::L; };   // back in time
+  auto fetch = [&](const Tile& t, int buf) {
+    if (t.k < filled) {
+      const int64_t row0 = first_row(t) + g * R;
+      const int c0 = t.cb * S::C + cl * V;
+      const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.f), static_cast<const T*>(p.dout)};
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const T* at = src[q] + row0 * p.W + c0;
+#pragma unroll
+        for (int i = 0; i < R; ++i, at += p.W) {
+          const bool in = c0 < p.W && row0 + i < limit;
+          copy_async(&sm.raw[buf][q][i][tid], in ? at : src[q], in);
+        }
+      }
+    }
+    copy_commit();
+  };
+  if (scout) {
+    for (int n = 0; n < 2; ++n) {
+      place(p, next_tile(p, n), sm.tile[n]);
+      if (sm.tile[n].k < filled) look_up<S>(p, first_row(sm.tile[n]), limit, sm.tile[n]);
+    }
+  }
+  __syncthreads();
+  Tile tile = sm.tile[0];
+  fetch(tile, 0);
+  fetch(sm.tile[1], 1);
+  if (tile.k < filled && tile.any) mark_rows<S>(p, first_row(tile), limit, tile.seq, sm.start[0], sm.end[0]);
+  __syncthreads();
+  int slot = 0;   // n % 3
+  for (int n = 0; tile.k < filled; ++n) {
+    const int buf = n & 1, slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+    const int64_t row0 = first_row(tile) + g * R;
+    const int c0 = tile.cb * S::C + cl * V;
+    const bool in = c0 < p.W;
+    int drawn = 0;
+    if (scout) drawn = next_tile(p, n + 2);
+    const int cf = tile.cb * S::C + tid % S::C;   // the thread's channel in the fold
+    const float ck = cf < p.W ? p.ck[static_cast<int64_t>(filled - 1 - tile.k) * p.W + cf] : 0.f;
+    copy_wait<1>();
+
+    // What the rows do to h, forward, and to the flow into the state before them, backward.
+    float2 a[R][U], A[U], H[U], cc[U];
+    int reset = 0, creset = 0;
+#pragma unroll
+    for (int e = 0; e < U; ++e) { A[e] = splat(1.f); H[e] = cc[e] = splat(0.f); }
+    auto rows_in = [&](auto marked) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
+        if constexpr (decltype(marked)::value) {
+          const int s = sm.start[buf][g * R + i];
+          if (s >= 0) {
+            reset = 1;
+#pragma unroll
+            for (int e = 0; e < U; ++e) H[e] = splat(0.f);
+            if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          float2 keep;
+          gates<T>(fr.pair(e), a[i][e], keep);
+          H[e] = fma2(a[i][e], H[e], TIED ? mul2(keep, xr.pair(e)) : xr.pair(e));
+          A[e] = mul2(A[e], a[i][e]);
+        }
+      }
+#pragma unroll
+      for (int i = R - 1; i >= 0; --i) {
+        const P dr = sm.raw[buf][2][i][tid];
+        if constexpr (decltype(marked)::value) {
+          const int s = sm.end[buf][g * R + i];
+          if (s >= 0) {
+            creset = 1;
+#pragma unroll
+            for (int e = 0; e < U; ++e) cc[e] = splat(0.f);
+            if (p.ds1 && in) load_f32<V>(p.ds1 + static_cast<int64_t>(s) * p.W + c0, cc);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) cc[e] = mul2(a[i][e], add2(dr.pair(e), cc[e]));
+      }
+    };
+    if (tile.any) rows_in(Yes{}); else rows_in(No{});
+    store_f32<V>(&sm.A[g][cl * V], A);
+    store_f32<V>(&sm.H[g][cl * V], H);
+    store_f32<V>(&sm.Cc[g][cl * V], cc);
+    if (cl == 0) {
+      sm.reset[g] = reset;
+      sm.creset[g] = creset;
+    }
+    if (scout) place(p, drawn, sm.tile[slot2]);
+    __syncthreads();
+    const Tile next = sm.tile[slot1];
+    fold_both<S>(p, sm, tile.k, tile.cb, ck, [&] {
+      if (next.k < filled && next.any)
+        mark_rows<S>(p, first_row(next), limit, next.seq, sm.start[buf ^ 1], sm.end[buf ^ 1]);
+      if (scout && sm.tile[slot2].k < filled) look_up<S>(p, first_row(sm.tile[slot2]), limit, sm.tile[slot2]);
+    });
+
+    if (in) {
+      float2 prev[R][U], h[U];
+      load_f32<V>(&sm.H[g][cl * V], h);
+      load_f32<V>(&sm.Cc[g][cl * V], cc);
+      const int64_t last = (row0 + R - 1) * p.W + c0;
+      T* dx = static_cast<T*>(p.dx) + last;
+      T* df = static_cast<T*>(p.df) + last;
+      auto rows_out = [&](auto marked) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if constexpr (decltype(marked)::value) {
+            const int s = sm.start[buf][g * R + i];
+            if (s >= 0) {
+#pragma unroll
+              for (int e = 0; e < U; ++e) h[e] = splat(0.f);
+              if (p.s0) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
+            }
+          }
+          const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            prev[i][e] = h[e];
+            if (i + 1 < R) {
+              float2 again, keep;
+              if (TIED) gates<T>(fr.pair(e), again, keep);
+              h[e] = fma2(a[i][e], h[e], TIED ? mul2(keep, xr.pair(e)) : xr.pair(e));
+            }
+          }
+        }
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i, dx -= p.W, df -= p.W) {
+          if constexpr (decltype(marked)::value) {
+            if (row0 + i >= limit) continue;
+            const int s = sm.end[buf][g * R + i];
+            if (s >= 0) {
+#pragma unroll
+              for (int e = 0; e < U; ++e) cc[e] = splat(0.f);
+              if (p.ds1) load_f32<V>(p.ds1 + static_cast<int64_t>(s) * p.W + c0, cc);
+            }
+          }
+          const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid], dr = sm.raw[buf][2][i][tid];
+          float2 ox[U], of[U];
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            float2 again, keep;
+            gates<T>(fr.pair(e), again, keep);
+            const float2 G1 = add2(dr.pair(e), cc[e]);
+            ox[e] = TIED ? mul2(keep, G1) : G1;
+            cc[e] = mul2(a[i][e], G1);
+            const float2 d = TIED ? fma2(xr.pair(e), splat(-1.f), prev[i][e]) : prev[i][e];
+            of[e] = mul2(mul2(keep, cc[e]), d);
+          }
+          *reinterpret_cast<P*>(dx) = P::from(ox);
+          *reinterpret_cast<P*>(df) = P::from(of);
+          if constexpr (decltype(marked)::value) {
+            const int s = sm.start[buf][g * R + i];
+            if (s >= 0 && p.ds0) store_f32<V>(p.ds0 + static_cast<int64_t>(s) * p.W + c0, cc);
+          }
+        }
+      };
+      if (tile.any) rows_out(Yes{}); else rows_out(No{});
+    }
+    fetch(sm.tile[slot2], buf);   // the buffer has been read to the end
+    tile = next;
+    slot = slot1;
+  }
+  copy_wait<0>();
 }
 
 template <typename T>
@@ -527,55 +867,73 @@ __global__ void __launch_bounds__(256) rec_step_kernel(const T* __restrict__ x, 
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const float xv = load_elem<T>(x, i);
-    const Gate g = gate_of(load_elem<T>(f, i));
-    const float h = fmaf(g.a, state[i], tied ? g.keep * xv : xv);
+    float2 a, keep;
+    gates<T>(make_float2(load_elem<T>(f, i), 0.f), a, keep);
+    const float h = fmaf(a.x, state[i], tied ? keep.x * xv : xv);
     state[i] = h;
     store_elem<T>(out, i, h);
   }
 }
 
-using ShapeB8 = Shape<uint16_t, 8, 8, 4>;    // 128 rows x 64 channels
-using ShapeF4 = Shape<float, 4, 16, 8>;      // 128 rows x 64 channels
-using ShapeB1 = Shape<uint16_t, 1, 32, 16>;  // 128 rows x 32 channels
-using ShapeF1 = Shape<float, 1, 32, 16>;
+using ForwardB = Shape<uint16_t, FSV, FSC, FSR>;
+using BackwardB = Shape<uint16_t, BSV, BSC, BSR>;
+using VectorF = Shape<float, 4, 8, 4>;       // 128 rows x 32 channels
+using ScalarB = Shape<uint16_t, 1, 32, 16>;  // 128 rows x 32 channels
+using ScalarF = Shape<float, 1, 32, 16>;
 
 bool vectors(int W, la_dtype dt) { return W % (dt == LA_BF16 ? 8 : 4) == 0; }
-int tile_channels(int W, la_dtype dt) { return vectors(W, dt) ? 64 : 32; }
-constexpr int kTileRows = 128;
 
-template <class S> cudaError_t launch_shape(const RecArgs& p, bool backward, cudaStream_t stream) {
-  static_assert(S::L == kTileRows, "workspace layout");
-  const unsigned grid = static_cast<unsigned>(p.ntiles) * static_cast<unsigned>(p.nblocks);
-  if (!backward) {
-    if (p.tied) rec_forward_kernel<S, true><<<grid, kThreads, 0, stream>>>(p);
-    else rec_forward_kernel<S, false><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (p.tied) rec_backward_kernel<S, true><<<grid, kThreads, 0, stream>>>(p);
-    else rec_backward_kernel<S, false><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Workspace: [error record] [ticket, flags (cleared for each call)] [tiles' (A, H)] [states after
-// the tiles] [a copy of the states that a call in place overwrites] [backward: checkpoints, for a
+template <class K> cudaError_t launch_kernel(K kernel, unsigned grid, size_t smem, const RecArgs& p, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <class S> cudaError_t launch_forward(RecArgs p, cudaStream_t stream) {
+  p.nblocks = (p.W + S::C - 1) / S::C;
+  const int64_t tiles = static_cast<int64_t>(p.ntiles) * p.nblocks, most = FB * static_cast<int64_t>(sm_count());
+  const unsigned grid = static_cast<unsigned>(tiles < most ? tiles : most);
+  const size_t smem = sizeof(Smem<S, 2, 2>);
+  return p.tied ? launch_kernel(rec_forward_kernel<S, true>, grid, smem, p, stream)
+                : launch_kernel(rec_forward_kernel<S, false>, grid, smem, p, stream);
+}
+template <class S> cudaError_t launch_backward(RecArgs p, cudaStream_t stream) {
+  p.nblocks = (p.W + S::C - 1) / S::C;
+  const int64_t tiles = static_cast<int64_t>(p.ntiles) * p.nblocks, most = BB * static_cast<int64_t>(sm_count());
+  const unsigned grid = static_cast<unsigned>(tiles < most ? tiles : most);
+  const size_t smem = sizeof(SmemBack<S, 3, 2>);
+  return p.tied ? launch_kernel(rec_backward_kernel<S, true>, grid, smem, p, stream)
+                : launch_kernel(rec_backward_kernel<S, false>, grid, smem, p, stream);
+}
+
+// Workspace: [error record] [ticket] [tiles' (A, H)] [states after the tiles] (these three set for
+// each walk) [a copy of the states that a call in place overwrites] [backward: checkpoints, for a
 // call that was given none].
 struct RecLayout {
-  int ntiles, nblocks;
+  int ntiles;
   size_t ctl, agg, inc, copy, ck, total;
 };
 RecLayout rec_layout(int nseq, int64_t tokens, int W, la_dtype dt, bool backward) {
   RecLayout l{};
-  const int C = tile_channels(W, dt);
-  l.ntiles = static_cast<int>((tokens + kTileRows - 1) / kTileRows);
-  l.nblocks = (W + C - 1) / C;
-  const size_t cells = static_cast<size_t>(l.ntiles) * l.nblocks * C;
-  l.ctl = up256(256 + sizeof(unsigned int) * (cells / 32));
-  l.agg = up256(sizeof(float2) * cells);
-  l.inc = up256(sizeof(float) * cells);
+  const size_t cols = (static_cast<size_t>(W) + 63) / 64 * 64;   // whole tiles of 32 or 64 channels
+  l.ntiles = static_cast<int>((tokens + kCkRows - 1) / kCkRows);
+  const size_t cells = l.ntiles * cols;
+  const bool chain = l.ntiles > 1;
+  l.ctl = 256;
+  l.agg = chain ? up256(sizeof(uint64_t) * cells) : 0;
+  l.inc = chain ? up256(sizeof(unsigned int) * cells) : 0;
   l.copy = up256(sizeof(float) * static_cast<size_t>(nseq) * W);
   l.ck = backward ? up256(sizeof(float) * static_cast<size_t>((tokens + kCkRows - 1) / kCkRows) * W) : 0;
   l.total = sizeof(ErrRec) + l.ctl + l.agg + l.inc + l.copy + l.ck;
@@ -587,11 +945,9 @@ cudaError_t launch_rec(RecArgs p, const RecLayout& l, la_dtype dt, bool backward
                        cudaStream_t stream) {
   char* base = static_cast<char*>(workspace) + sizeof(ErrRec);
   p.ntiles = l.ntiles;
-  p.nblocks = l.nblocks;
   p.ticket = reinterpret_cast<unsigned int*>(base);
-  p.flags = reinterpret_cast<unsigned int*>(base + 256);
-  p.agg = reinterpret_cast<float2*>(base + l.ctl);
-  p.inc = reinterpret_cast<float*>(base + l.ctl + l.agg);
+  p.agg = reinterpret_cast<uint64_t*>(base + l.ctl);
+  p.inc = reinterpret_cast<unsigned int*>(base + l.ctl + l.agg);
   // Where the states are updated in place, a tile may write what another still reads: from a copy.
   const float*& from = backward ? p.ds1 : p.s0;
   const float* to = backward ? p.ds0 : p.s1;
@@ -609,11 +965,14 @@ cudaError_t launch_rec(RecArgs p, const RecLayout& l, la_dtype dt, bool backward
     e = cudaMemcpyAsync(copy, from, bytes, cudaMemcpyDeviceToDevice, stream);
     from = copy;
   }
-  if (e == cudaSuccess && l.ntiles > 1) e = cudaMemsetAsync(p.ticket, 0, l.ctl, stream);
+  if (e == cudaSuccess && l.ntiles > 1) e = cudaMemsetAsync(p.ticket, 0xFF, l.ctl + l.agg + l.inc, stream);
   if (e != cudaSuccess) return e;
-  if (dt == LA_BF16)
-    return vectors(p.W, dt) ? launch_shape<ShapeB8>(p, backward, stream) : launch_shape<ShapeB1>(p, backward, stream);
-  return vectors(p.W, dt) ? launch_shape<ShapeF4>(p, backward, stream) : launch_shape<ShapeF1>(p, backward, stream);
+  const bool vec = vectors(p.W, dt);
+  if (backward)
+    return dt == LA_BF16 ? (vec ? launch_backward<BackwardB>(p, stream) : launch_backward<ScalarB>(p, stream))
+                         : (vec ? launch_backward<VectorF>(p, stream) : launch_backward<ScalarF>(p, stream));
+  return dt == LA_BF16 ? (vec ? launch_forward<ForwardB>(p, stream) : launch_forward<ScalarB>(p, stream))
+                       : (vec ? launch_forward<VectorF>(p, stream) : launch_forward<ScalarF>(p, stream));
 }
 
 la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspace, size_t ws_bytes, bool backward,
@@ -640,7 +999,8 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
     if (s && !aligned16(s)) return LA_ERR_INVALID_ARG;
   const RecLayout l = rec_layout(p.nseq, p.tokens, p.W, dt, backward);
   if (!workspace || !aligned256(workspace) || ws_bytes < l.total) return LA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(l.ntiles) * l.nblocks > INT32_MAX) return LA_ERR_UNSUPPORTED;
+  // tickets count tiles of 32 channels and are drawn two ahead by every CTA
+  if (static_cast<int64_t>(l.ntiles) * ((p.W + 31) / 32) > INT32_MAX - 65536) return LA_ERR_UNSUPPORTED;
   p.err = static_cast<ErrRec*>(workspace);
   p.tied = mode == LA_INPUT_TIED;
   cudaError_t e = cudaSuccess;
