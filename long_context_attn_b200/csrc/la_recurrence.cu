@@ -2,20 +2,19 @@
 // by channel: forward, one-token step and backward (sm_100a).
 //
 // Rows t .. u of a channel act on the state that enters them as h -> A h + H, A the product of
-// their gates; two neighbours compose to (A2 A1, A2 H1 + H2).  The packed rows are cut into
-// tiles of L rows x C channels, one CTA each, and a tile is read once: every thread folds its R
-// rows x V channels in registers, the CTA folds the threads, the tile's (A, H) is published,
-// the state entering the tile is found from the tiles before it, and the threads walk their rows
-// again from the states that enter them.  A row that starts a sequence takes its state from
-// state_in instead, so packed sequences need no tiles of their own and cut the dependence.
+// their gates; two neighbours compose to (A2 A1, A2 H1 + H2).  A CTA walks C channels of the
+// packed rows in tiles of L rows, reading each once.  In a tile a thread takes R rows of two
+// channels and folds them to (A, H), keeping their a and b in registers; the groups of a warp
+// compose with shuffles, the warps through shared memory, and every thread folds all warps
+// from the state that entered the tile, so that it has both the state entering its own rows and the
+// one entering the next tile: one barrier a tile.  Then it walks its rows again and writes them.  A row
+// that starts a sequence takes its state from state_in instead, so packed sequences need no CTAs of
+// their own.
 //
-// State entering a tile: tiles are handed out in time order by a ticket, so every tile before
-// one that is worked on has been started and never waits for a later one.  A warp looks back over
-// the tiles before its own until it finds one whose state after the last row is known, and folds
-// the (A, H) between from there, oldest first.  Values and their being there are one word, read
-// and written whole, so the chain needs no flags and no fences.  That fold does the same operations in the same
-// order as the tiles' own (h <- A h + H, tile by tile), so the result does not depend on how
-// far the warp had to look.
+// Where the channels are too few to fill the GPU, a cluster of up to 16 CTAs walks them together,
+// each CTA a tile of the round's.  The CTAs put the (A, H) of their tiles into one another's shared
+// memory and meet at the cluster's barrier; then every thread folds the round's tiles as it folds
+// the warps.  No CTA waits for another in any other way, and the result is the same in every run.
 //
 // The backward walks time in reverse: with c_t = a_t (dout_t + c_{t+1}) what flows into the
 // state before row t, rows act on the c that enters them from behind as c -> A c + C with the same
@@ -29,23 +28,8 @@ void set_last_path(const char* path);
 namespace {
 
 constexpr int kCkRows = LA_RECURRENCE_CHECKPOINT_ROWS;
-constexpr int kThreads = 256;
-#ifndef FB
-#define FB 2
-#endif
-#ifndef BB
-#define BB 2
-#endif
-#ifndef FSV
-#define FSV 8
-#define FSC 8
-#define FSR 4
-#endif
-#ifndef BSV
-#define BSV 4
-#define BSC 8
-#define BSR 4
-#endif
+constexpr int kMaxCluster = 16;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 struct RecArgs {
   const void *x, *f, *dout;
@@ -56,44 +40,49 @@ struct RecArgs {
   int nseq, T, W, tied;
   int64_t tokens;
   ErrRec* err;
-  // Chain between the tiles (more than one in time): all bits set before each walk.
-  int ntiles, nblocks;          // in time, across the channels
-  unsigned int* ticket;         // [0]: the last tile handed out; [1]: kOpen, until a wait ran out
-  uint64_t* agg;                // [ntiles][nblocks * C]: (A, H) of the tile
-  unsigned int* inc;            // [ntiles][nblocks * C]: state after the tile
+  int nblocks;   // across the channels
 };
-// What a word of the chain holds until its value is there: a NaN that is never published.
-constexpr unsigned int kOpen = 0xFFFFFFFFu;
 
-// Two fp32 operations in one instruction (each rounded as the single one).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+// Two fp32 values in one 64-bit register, and two operations in one instruction (each rounded as the
+// single one).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 make_f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
   return d;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
-      " fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return d;
 }
-__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ F2 splat(float v) { return make_f2(v, v); }
 
 // a = sigmoid(f) = 1 / (1 + t) and keep = 1 - a = t / (1 + t) with t = exp(-f), neither by
 // cancellation.  Two special-function operations an element, exp2 and the reciprocal, which the
 // memory rate leaves room for.  bf16 gates take exp2 of the rounded product -f log2(e): t is
 // then off by at most (4 + |f|) 2^-24, against the 2^-9 the gate itself is rounded to (with expf
 // and an IEEE division the first tiled kernel spent 47 instructions an element and ran at 0.30
-// of the HBM rate, instruction-bound); fp32 gates call expf.  a is 0 where t leaves fp32's
-// normal range (f < -87.3), and keep, which t a would not give there, is 1.
+// of the HBM rate, instruction-bound); fp32 gates call expf.  t is held to 2^126 (f < -87.3), so
+// that 1 / (1 + t) stays a normal number and keep = 1 there; taking 2^-126 away from it makes a 0
+// there and changes no a above 2^-101.  A NaN passes.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -104,146 +93,138 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-template <typename T> __device__ __forceinline__ void gates(float2 f, float2& a, float2& keep) {
-  float2 t;
+__device__ __forceinline__ float min_nan(float x, float most) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+  return y;
+}
+template <typename T> __device__ __forceinline__ void gates(F2 f, F2& a, F2& keep) {
+  F2 t;
   if constexpr (sizeof(T) == 2) {
-    const float2 y = mul2(f, splat(-1.4426950408889634f));
-    t = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    const float2 y = split(mul2(f, splat(-1.4426950408889634f)));
+    t = make_f2(exp2_approx(min_nan(y.x, 126.0f)), exp2_approx(min_nan(y.y, 126.0f)));
   } else {
-    t = make_float2(expf(-f.x), expf(-f.y));
+    const float2 v = split(f);
+    t = make_f2(min_nan(expf(-v.x), 0x1p126f), min_nan(expf(-v.y), 0x1p126f));
   }
-  const float2 d = add2(t, splat(1.0f));
-  a = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  const float2 k = mul2(t, a);
-  keep = make_float2(a.x == 0.0f ? 1.0f : k.x, a.y == 0.0f ? 1.0f : k.y);
+  const float2 d = split(add2(t, splat(1.0f)));
+  a = make_f2(rcp_approx(d.x), rcp_approx(d.y));
+  keep = mul2(t, a);
+  a = add2(a, splat(-0x1p-126f));
 }
 
-// V consecutive channels of one row, as loaded; they are worked on in pairs (V = 1: with an idle
-// second half).
-template <typename T, int V> struct Pack;
-template <> struct Pack<uint16_t, 8> {
-  uint4 r;
-  __device__ __forceinline__ float2 pair(int i) const {
-    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-  __device__ __forceinline__ static Pack from(const float2* o) {
-    return Pack{make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y), pack_bf16x2(o[2].x, o[2].y),
-                           pack_bf16x2(o[3].x, o[3].y))};
-  }
-};
-template <> struct Pack<uint16_t, 4> {
-  uint2 r;
-  __device__ __forceinline__ float2 pair(int i) const {
-    const uint32_t w = i == 0 ? r.x : r.y;
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-  __device__ __forceinline__ static Pack from(const float2* o) {
-    return Pack{make_uint2(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y))};
-  }
-};
-template <> struct Pack<float, 4> {
-  float4 r;
-  __device__ __forceinline__ float2 pair(int i) const { return i == 0 ? make_float2(r.x, r.y) : make_float2(r.z, r.w); }
-  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{make_float4(o[0].x, o[0].y, o[1].x, o[1].y)}; }
-};
-template <> struct Pack<uint16_t, 1> {
-  uint16_t r;
-  __device__ __forceinline__ float2 pair(int) const { return make_float2(bf16_bits_to_f32(r), 0.f); }
-  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{f32_to_bf16_bits(o[0].x)}; }
-};
-template <> struct Pack<float, 1> {
-  float r;
-  __device__ __forceinline__ float2 pair(int) const { return make_float2(r, 0.f); }
-  __device__ __forceinline__ static Pack from(const float2* o) { return Pack{o[0].x}; }
-};
-// V fp32 values of the states, the checkpoints or the folds.
-template <int V> __device__ __forceinline__ void load_f32(const float* p, float2* o) {
-  if constexpr (V == 1) {
-    o[0] = make_float2(*p, 0.f);
+// A thread's two channels of one row in shared memory.
+__device__ __forceinline__ F2 load_pair(const uint16_t* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 load_pair(const float* p) { return *reinterpret_cast<const F2*>(p); }
+
+// Two channels in global memory, the first at c; VEC: rows are aligned to pairs and whole pairs are
+// inside (c < W).  Otherwise one by one, those that are.
+template <bool VEC> __device__ __forceinline__ F2 load_state(const float* p, int c, int W) {
+  if constexpr (VEC) return *reinterpret_cast<const F2*>(p);
+  return make_f2(p[0], c + 1 < W ? p[1] : 0.f);
+}
+template <bool VEC> __device__ __forceinline__ void store_pair(float* p, F2 pair, int c, int W) {
+  if constexpr (VEC) {
+    *reinterpret_cast<F2*>(p) = pair;
   } else {
+    const float2 v = split(pair);
+    p[0] = v.x;
+    if (c + 1 < W) p[1] = v.y;
+  }
+}
+template <bool VEC> __device__ __forceinline__ void store_pair(uint16_t* p, F2 pair, int c, int W) {
+  if constexpr (VEC) {
+    const float2 v = split(pair);
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
+  } else {
+    const float2 v = split(pair);
+    p[0] = f32_to_bf16_bits(v.x);
+    if (c + 1 < W) p[1] = f32_to_bf16_bits(v.y);
+  }
+}
+
+// CL threads side by side take two channels each; the G groups of a CTA, GW in a warp, take R rows each.
+// VEC: rows are made of whole 16-byte vectors.
+template <typename T_, int CL_, int R_, bool VEC_> struct Shape {
+  using T = T_;
+  static constexpr int CL = CL_, C = 2 * CL, GW = 32 / CL, G = kWarps * GW, R = R_, L = G * R;
+  static constexpr bool VEC = VEC_;
+  static_assert(L % kCkRows == 0 && kCkRows % R == 0, "a tile starts at a checkpoint, which a thread's first row may be");
+};
+
+template <class S, int NT> struct Smem {
+  typename S::T raw[2][NT][S::L][S::C];   // of this tile and the next; each warp's rows are its own
+  float A[2][kWarps][S::C], H[2][kWarps][S::C];
+  int cut[2][kWarps];                     // whether a sequence starts in the warp's rows
+  int start[S::L], end[S::L];             // of a tile with marks: the sequence that starts (ends) at a row, or -1
+  float tA[2][kMaxCluster][S::C], tH[2][kMaxCluster][S::C];   // of the round's tiles, each put here by its CTA
+  int tcut[2][kMaxCluster];
+};
+// The backward's: the same for what flows back, beside the states forward in the tile.
+template <class S> struct SmemBack : Smem<S, 3> {
+  float Cc[2][kWarps][S::C];
+  int ccut[2][kWarps];
+};
+
+// A warp's rows of a tile into shared memory, not waited for; zeros outside the rows and channels.
+template <class S, int NT>
+__device__ __forceinline__ void fetch_rows(const RecArgs& p, Smem<S, NT>& sm, int buf, int64_t r0, int c0, int64_t limit) {
+  using T = typename S::T;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.f), static_cast<const T*>(p.dout)};
+  constexpr int kWarpRows = S::L / kWarps;
+  if constexpr (S::VEC) {
+    constexpr int kVec = 16 / sizeof(T), kPer = S::C / kVec, kStep = 32 / kPer;   // lanes a row, rows at once
+    const int r = warp * kWarpRows + lane / kPer, c = lane % kPer * kVec;
+    const bool col = c0 + c < p.W, all = r0 + S::L <= limit;
+    if (all && !col) return;   // zero since the beginning
+    const int64_t step = static_cast<int64_t>(kStep) * p.W;
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 t = *reinterpret_cast<const float4*>(p + i);
-      o[i / 2] = make_float2(t.x, t.y);
-      o[i / 2 + 1] = make_float2(t.z, t.w);
+    for (int q = 0; q < NT; ++q) {
+      const T* at = src[q] + (r0 + r) * p.W + c0 + c;
+      const unsigned int d = static_cast<unsigned int>(__cvta_generic_to_shared(&sm.raw[buf][q][r][c]));
+#pragma unroll
+      for (int i = 0; i < kWarpRows; i += kStep, at += step) {
+        if (all) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * S::C * static_cast<int>(sizeof(T))), "l"(at)
+                       : "memory");
+        } else {
+          const bool in = col && r0 + r + i < limit;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + i * S::C * static_cast<int>(sizeof(T))),
+                       "l"(in ? at : src[q]), "r"(in ? 16 : 0) : "memory");
+        }
+      }
+    }
+  } else {   // element by element, waited for
+#pragma unroll 1
+    for (int q = 0; q < NT; ++q) {
+#pragma unroll 1
+      for (int i = 0; i < kWarpRows; ++i) {
+        const int r = warp * kWarpRows + i;
+        for (int c = lane; c < S::C; c += 32)
+          sm.raw[buf][q][r][c] = c0 + c < p.W && r0 + r < limit ? src[q][(r0 + r) * p.W + c0 + c] : T(0);
+      }
     }
   }
 }
-template <int V> __device__ __forceinline__ void store_f32(float* p, const float2* o) {
-  if constexpr (V == 1) {
-    *p = o[0].x;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(o[i / 2].x, o[i / 2].y, o[i / 2 + 1].x, o[i / 2 + 1].y);
-  }
+// Zeros the buffers' columns outside the channels, which fetch_rows() then leaves alone (the caller's
+// barrier follows).
+template <class S, int NT> __device__ __forceinline__ void zero_columns(const RecArgs& p, Smem<S, NT>& sm, int c0) {
+  if (!S::VEC || c0 + S::C <= p.W) return;
+  using T = typename S::T;
+  T* raw = &sm.raw[0][0][0][0];
+  for (int i = threadIdx.x; i < 2 * NT * S::L * S::C; i += kThreads)
+    if (c0 + i % S::C >= p.W) raw[i] = T(0);
 }
-
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
-
-// CL threads side by side take V channels each; G = 256 / CL groups of them take R rows each.
-template <typename T_, int V_, int CL_, int R_> struct Shape {
-  using T = T_;
-  static constexpr int V = V_, CL = CL_, R = R_, U = (V + 1) / 2;   // U pairs
-  static constexpr int C = CL * V, G = kThreads / CL, L = G * R;
-  static constexpr int NP = kThreads / C, GP = G / NP;   // the fold over groups: NP threads a channel
-  static_assert(C % 32 == 0 && kThreads % C == 0 && G % NP == 0 && L == kCkRows, "tile");
-};
-
-// A tile: its place in the walk and across the channels, whether a sequence starts or ends in its
-// rows (or they end), and the sequence of its first row (the first that ends behind it).
-struct Tile {
-  int k, cb, any, seq;
-};
-
-template <class S, int NT, int NB> struct Smem {
-  Pack<typename S::T, S::V> raw[NB][NT][S::R][kThreads];   // each thread's own, as the copies bring them
-  float A[S::G][S::C], H[S::G][S::C];     // of each group; then H: the state entering it
-  float pA[S::NP][S::C], pH[S::NP][S::C];
-  float in[S::C];
-  int start[2][S::L], end[2][S::L];       // of a tile with `any`: the sequence that starts (ends) at a row, or -1
-  int reset[S::G], preset[S::NP];
-  Tile tile[3];
-};
-// The backward's: the same for the walk back (C, cin, creset) beside the walk forward in the tile.
-template <class S, int NT, int NB> struct SmemBack : Smem<S, NT, NB> {
-  float Cc[S::G][S::C], pC[S::NP][S::C], cin[S::C];
-  int creset[S::G], cpreset[S::NP];
-};
-
-// One vector into shared memory without waiting for it; zeros where `in` is false.
-template <typename P> __device__ __forceinline__ void copy_async(P* dst, const void* src, bool in) {
-  const unsigned int d = static_cast<unsigned int>(__cvta_generic_to_shared(dst));
-  if constexpr (sizeof(P) == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
-  else if constexpr (sizeof(P) == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(in ? 8 : 0) : "memory");
-  else
-    *dst = in ? *static_cast<const P*>(src) : P{};   // single elements: waited for
+__device__ __forceinline__ void commit_rows() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The warp's rows of the tile fetched before the last one are there.
+__device__ __forceinline__ void rows_here() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncwarp();
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ unsigned int load_relaxed(const unsigned int* p) {
-  unsigned int v;
-  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint64_t load_relaxed(const uint64_t* p) {
-  uint64_t v;
-  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void store_relaxed(unsigned int* p, unsigned int v) {
-  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-__device__ __forceinline__ void store_relaxed(uint64_t* p, uint64_t v) {
-  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-// The bits of a value of the chain: any NaN as the one that is not kOpen.
-__device__ __forceinline__ unsigned int published(float v) { return v == v ? __float_as_uint(v) : 0x7FC00000u; }
 
 // Rows of the packed batch that belong to a sequence: the first `limit` ones.
 __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
@@ -252,54 +233,45 @@ __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
   return n < 0 ? 0 : n < p.tokens ? n : p.tokens;
 }
 
-// Completes a tile (one thread).  Without `any`, every row of the tile is in one sequence and none
-// is its first or last.
-template <class S> __device__ __forceinline__ void look_up(const RecArgs& p, int64_t r0, int64_t limit, Tile& t) {
-  constexpr int L = S::L;
+// The sequence a row is in: the first that ends behind the row.
+struct Sequence {
+  int s;
+  int64_t lo, hi;
+};
+__device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, int from) {
+  Sequence q;
   if (!p.cu) {
-    const unsigned int T = p.T, row = static_cast<unsigned int>(r0), s = row / T, in = row - s * T;
-    t.seq = static_cast<int>(s);
-    t.any = in == 0 || static_cast<int64_t>(in) + L >= T || r0 + L > limit;
-    return;
+    q.s = static_cast<int>(static_cast<unsigned int>(row) / static_cast<unsigned int>(p.T));   // row < tokens <= INT32_MAX
+    q.lo = static_cast<int64_t>(q.s) * p.T;
+    q.hi = q.lo + p.T;
+    return q;
   }
-  int lo = 0, hi = p.nseq;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu + mid + 1) > r0) hi = mid; else lo = mid + 1;
+  int a = from, b = p.nseq;
+  while (a < b) {
+    const int mid = (a + b) >> 1;
+    if (__ldg(p.cu + mid + 1) > row) b = mid; else a = mid + 1;
   }
-  t.seq = lo;
-  t.any = lo >= p.nseq || __ldg(p.cu + lo) >= r0 || __ldg(p.cu + lo + 1) <= r0 + L || r0 + L > limit;
+  q.s = a;
+  q.lo = a < p.nseq ? __ldg(p.cu + a) : p.tokens;
+  q.hi = a < p.nseq ? __ldg(p.cu + a + 1) : p.tokens;
+  return q;
 }
-
-// Marks the rows of a tile with `any` where sequences start and end (a thread a row).
+// Marks the tile's rows where sequences start and end.
 template <class S>
-__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int seq, int* start, int* end) {
-  const int tid = threadIdx.x;
-  if (tid >= S::L) return;
-  const int64_t row = r0 + tid;
-  int st = -1, en = -1;
-  if (row < limit) {
-    if (!p.cu) {
-      const unsigned int T = p.T, s = static_cast<unsigned int>(row) / T, in = static_cast<unsigned int>(row) - s * T;
-      if (in == 0) st = static_cast<int>(s);
-      if (in == T - 1) en = static_cast<int>(s);
-    } else {
-      int a = seq, b = p.nseq;   // the sequence of this row
-      while (a < b) {
-        const int mid = (a + b) >> 1;
-        if (__ldg(p.cu + mid + 1) > row) b = mid; else a = mid + 1;
-      }
-      if (a < p.nseq) {
-        const int64_t first = __ldg(p.cu + a), last = static_cast<int64_t>(__ldg(p.cu + a + 1)) - 1;
-        if (first >= 0 && first <= row && last < p.tokens) {
-          if (first == row) st = a;
-          if (last == row) en = a;
-        }
+__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int from, int* start, int* end) {
+  for (int i = threadIdx.x; i < S::L; i += kThreads) {
+    const int64_t row = r0 + i;
+    int st = -1, en = -1;
+    if (row < limit) {
+      const Sequence q = sequence_of(p, row, from);
+      if (q.s < p.nseq && q.lo >= 0 && q.lo <= row && q.hi <= p.tokens) {
+        if (q.lo == row) st = q.s;
+        if (q.hi - 1 == row) en = q.s;
       }
     }
+    start[i] = st;
+    end[i] = en;
   }
-  start[tid] = st;
-  end[tid] = en;
 }
 
 // Sequences without rows: their final state (gradient) is the initial (final) one.  Malformed
@@ -317,547 +289,389 @@ __device__ __forceinline__ void rowless_sequences(const RecArgs& p, const float*
   }
 }
 
-// One warp, 32 channels, `col` the lane's: what enters the walk's tile k (> 0).
-__device__ __forceinline__ float look_back(const RecArgs& p, int k, int64_t col, int64_t cols) {
-  constexpr int K = 8;   // tiles looked at in one trip to L2
-  uint64_t t0 = 0;
-  int base = k - 1;
-  float h = 0.f;
-  for (unsigned int polls = 0;;) {
-    unsigned int inc[K], known = 0, there = 0;
-    uint64_t agg[K];
-#pragma unroll
-    for (int u = 0; u < K; ++u) {
-      const int i = base - u < 0 ? 0 : base - u;
-      inc[u] = load_relaxed(p.inc + i * cols + col);
-      agg[u] = load_relaxed(p.agg + i * cols + col);
-    }
-#pragma unroll
-    for (int u = 0; u < K; ++u) {
-      known |= static_cast<unsigned int>(inc[u] != kOpen) << u;
-      there |= static_cast<unsigned int>(static_cast<unsigned int>(agg[u]) != kOpen) << u;
-    }
-    known = __reduce_and_sync(0xffffffffu, known);
-    there = __reduce_and_sync(0xffffffffu, there);
-    const unsigned int near = known ? (known & (0u - known)) - 1u : (1u << K) - 1u;   // tiles nearer than a known one
-    if ((there & near) == near) {
-      if (!known) {
-        base -= K;   // all (A, H) there: look further back
-        continue;
-      }
-      // the known state, then the tiles of this window behind it, oldest first
-#pragma unroll
-      for (int u = K - 1; u >= 0; --u) {
-        if (near >> u & 1u)
-          h = fmaf(__uint_as_float(static_cast<unsigned int>(agg[u])), h,
-                   __uint_as_float(static_cast<unsigned int>(agg[u] >> 32)));
-        else if (known >> u & 1u)
-          h = __uint_as_float(inc[u]);
-      }
-      break;
-    }
-    if ((++polls & 63u) == 0) {   // no progress: has somebody given up, or is it time to?
-      if (load_relaxed(p.ticket + 1) != kOpen) return 0.f;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > wait_limit_ns(p.err)) {
-        if ((threadIdx.x & 31) == 0) {
-          report(p.err, LA_ERR_TIMEOUT, SITE_RECURRENCE_CHAIN, static_cast<unsigned>(k), static_cast<unsigned>(col));
-          store_relaxed(p.ticket + 1, 0u);
-        }
-        return 0.f;
-      }
-    }
-  }
-  for (int i = base + 1; i < k; i += K) {   // the windows passed on the way
-    uint64_t t[K];
-#pragma unroll
-    for (int u = 0; u < K; ++u) t[u] = load_relaxed(p.agg + (i + u) * cols + col);
-#pragma unroll
-    for (int u = 0; u < K; ++u)
-      h = fmaf(__uint_as_float(static_cast<unsigned int>(t[u])), h, __uint_as_float(static_cast<unsigned int>(t[u] >> 32)));
-  }
-  return h;
+template <bool VEC> __device__ __forceinline__ F2 state_or_zero(const float* states, int s, int c0, int W) {
+  return states ? load_state<VEC>(states + static_cast<int64_t>(s) * W + c0, c0, W) : splat(0.f);
 }
 
-// What the chain knows of the walk's tile k is (tA, tH), with `cut` set where a sequence starts
-// in it, so that what enters it does not leave it: published; returns what enters the tile.
-// `meanwhile` runs before the wait.  One warp, 32 channels, `col` the lane's.
-template <class F>
-__device__ __forceinline__ float chain(const RecArgs& p, int k, int64_t col, int64_t cols, float tA, float tH, int cut,
-                                       F meanwhile) {
-  if (p.ntiles == 1) {
-    meanwhile();
-    return 0.f;
+// Acts on h as a run of rows with (A, H) does; `cut`: a sequence starts in the run, so what enters it
+// does not leave it (and is not multiplied by 0: it may be infinite).
+__device__ __forceinline__ F2 act(int cut, F2 A, F2 H, F2 h) { return cut ? H : fma2(A, h, H); }
+
+__device__ __forceinline__ F2 shift(F2 pair, int d, bool up) {
+  const float2 v = split(pair);
+  return up ? make_f2(__shfl_up_sync(0xffffffffu, v.x, d), __shfl_up_sync(0xffffffffu, v.y, d))
+            : make_f2(__shfl_down_sync(0xffffffffu, v.x, d), __shfl_down_sync(0xffffffffu, v.y, d));
+}
+// Composes the groups of a warp: (A, H, cut) of the lane's group becomes that of it and all groups
+// before it (BACK: behind it), and (eA, eH, ecut) is that of those without it.
+template <int CL, bool BACK>
+__device__ __forceinline__ void compose_warp(F2& A, F2& H, int& cut, F2& eA, F2& eH, int& ecut) {
+  const int gw = (threadIdx.x & 31) / CL, g = BACK ? 32 / CL - 1 - gw : gw;
+#pragma unroll
+  for (int d = 1; d < 32 / CL; d *= 2) {
+    const F2 uA = shift(A, d * CL, !BACK), uH = shift(H, d * CL, !BACK);
+    const int ucut = BACK ? __shfl_down_sync(0xffffffffu, cut, d * CL) : __shfl_up_sync(0xffffffffu, cut, d * CL);
+    if (g >= d) {
+      H = act(cut, A, H, uH);
+      A = mul2(A, uA);
+      cut |= ucut;
+    }
   }
-  if (cut || k == 0)
-    store_relaxed(p.inc + k * cols + col, published(tH));
-  else
-    store_relaxed(p.agg + k * cols + col, static_cast<uint64_t>(published(tH)) << 32 | published(tA));
-  meanwhile();
-  if (k == 0) return 0.f;   // nothing enters the first tile
-  const float in = look_back(p, k, col, cols);
-  if (!cut) store_relaxed(p.inc + k * cols + col, published(fmaf(tA, in, tH)));
-  return in;
+  eA = splat(1.f);
+  eH = splat(0.f);
+  ecut = 0;
+  if constexpr (CL < 32) {
+    const F2 uA = shift(A, CL, !BACK), uH = shift(H, CL, !BACK);
+    const int ucut = BACK ? __shfl_down_sync(0xffffffffu, cut, CL) : __shfl_up_sync(0xffffffffu, cut, CL);
+    if (g > 0) {
+      eA = uA;
+      eH = uH;
+      ecut = ucut;
+    }
+  }
 }
 
-// Acts on h as a run of rows with (A, H) does; `cut`: what enters the run does not leave it (and
-// is not multiplied by 0: it may be infinite).
-__device__ __forceinline__ float act(int cut, float A, float H, float h) { return cut ? H : fmaf(A, h, H); }
+// The cluster's CTAs.
+__device__ __forceinline__ unsigned int cluster_rank() {
+  unsigned int r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned int cluster_size() {
+  unsigned int n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores into the shared memory of CTA `rank` at the place that `p` is of this one.
+__device__ __forceinline__ unsigned int there(const void* p, unsigned int rank) {
+  unsigned int r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<unsigned int>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void put(const float* p, unsigned int rank, F2 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(there(p, rank)), "l"(v.v) : "memory");
+}
+__device__ __forceinline__ void put(const int* p, unsigned int rank, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there(p, rank)), "r"(v) : "memory");
+}
 
-// The fold over the CTA's groups and, through the chain, over the tiles before it.  On entry sm.A,
-// sm.H, sm.reset hold each group's (A, H) and whether a sequence starts in it; on return sm.H[g]
-// is what enters group g.  `meanwhile` runs once in every thread, before the wait.
-template <class S, class M, class F>
-__device__ __forceinline__ void fold_forward(const RecArgs& p, M& sm, int k, int cb, F meanwhile) {
-  constexpr int C = S::C, NP = S::NP, GP = S::GP;
-  const int c = threadIdx.x % C, part = threadIdx.x / C;
-  float A[GP], H[GP];
-  float pa = 1.f, ph = 0.f;
-  int pr = 0;
+// Once every warp's (A, H) is in shared memory (H and cut: of the walk's direction): what enters this
+// warp's rows, from what enters the round's tiles, `state`, which becomes what leaves them.
+template <class S, bool CLUSTER, bool BACK, bool MARKED, class M>
+__device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C], const int* cut, int cl, F2& state) {
+  const int warp = threadIdx.x >> 5;
+  if constexpr (!CLUSTER) {
+    F2 h = state;
 #pragma unroll
-  for (int i = 0; i < GP; ++i) {
-    const int g = part * GP + i, r = sm.reset[g];
-    A[i] = sm.A[g][c];
-    H[i] = sm.H[g][c];
-    ph = act(r, A[i], H[i], ph);
-    pa *= A[i];
-    pr |= r;
-  }
-  sm.pA[part][c] = pa;
-  sm.pH[part][c] = ph;
-  if (c == 0) sm.preset[part] = pr;
-  __syncthreads();
-  if (part == 0) {   // whole warps: C is a multiple of 32
-    float tA = 1.f, tH = 0.f;
-    int cut = 0;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      tH = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], tH);
-      tA *= sm.pA[i][c];
-      cut |= sm.preset[i];
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = BACK ? kWarps - 1 - i : i;
+      if (w == warp) h = state;
+      state = act(MARKED ? cut[w] : 0, load_pair(&sm.A[buf][w][2 * cl]), load_pair(&H[w][2 * cl]), state);
     }
-    sm.in[c] = chain(p, k, static_cast<int64_t>(cb) * C + c, static_cast<int64_t>(p.nblocks) * C, tA, tH, cut, meanwhile);
+    return h;
   } else {
-    meanwhile();
-  }
-  __syncthreads();
-  float h = sm.in[c];
+    // the tile's (A, H), and that of the warps before this one
+    F2 tA = splat(1.f), tH = splat(0.f), bA = tA, bH = tH;
+    int tcut = 0, bcut = 0;
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    if (i < part) h = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], h);
-#pragma unroll
-  for (int i = 0; i < GP; ++i) {
-    const int g = part * GP + i;
-    sm.H[g][c] = h;
-    h = act(sm.reset[g], A[i], H[i], h);
-  }
-  __syncthreads();
-}
-
-// The backward's folds, both at once: forward in the tile from the checkpoint `ck` (the thread's
-// channel's), and from the last group to the first, through the chain, of what flows back:
-// on return sm.H[g] and sm.Cc[g] are what enters group g from before and from behind.
-template <class S, class M, class F>
-__device__ __forceinline__ void fold_both(const RecArgs& p, M& sm, int k, int cb, float ck, F meanwhile) {
-  constexpr int C = S::C, NP = S::NP, GP = S::GP;
-  const int c = threadIdx.x % C, part = threadIdx.x / C;
-  float A[GP], H[GP], Cc[GP];
-  float pa = 1.f, ph = 0.f, pc = 0.f;
-  int pr = 0, pe = 0;
-#pragma unroll
-  for (int i = 0; i < GP; ++i) {
-    const int g = part * GP + i, r = sm.reset[g];
-    A[i] = sm.A[g][c];
-    H[i] = sm.H[g][c];
-    Cc[i] = sm.Cc[g][c];
-    ph = act(r, A[i], H[i], ph);
-    pa *= A[i];
-    pr |= r;
-  }
-#pragma unroll
-  for (int i = GP - 1; i >= 0; --i) {
-    const int e = sm.creset[part * GP + i];
-    pc = act(e, A[i], Cc[i], pc);
-    pe |= e;
-  }
-  sm.pA[part][c] = pa;
-  sm.pH[part][c] = ph;
-  sm.pC[part][c] = pc;
-  if (c == 0) {
-    sm.preset[part] = pr;
-    sm.cpreset[part] = pe;
-  }
-  __syncthreads();
-  if (part == 0) {
-    float tA = 1.f, tC = 0.f;
-    int cut = 0;
-#pragma unroll
-    for (int i = NP - 1; i >= 0; --i) {
-      tC = act(sm.cpreset[i], sm.pA[i][c], sm.pC[i][c], tC);
-      tA *= sm.pA[i][c];
-      cut |= sm.cpreset[i];
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = BACK ? kWarps - 1 - i : i, r = MARKED ? cut[w] : 0;
+      if (w == warp) { bA = tA; bH = tH; bcut = tcut; }
+      const F2 wA = load_pair(&sm.A[buf][w][2 * cl]);
+      tH = act(r, wA, load_pair(&H[w][2 * cl]), tH);
+      tA = mul2(tA, wA);
+      tcut |= r;
     }
-    sm.cin[c] = chain(p, k, static_cast<int64_t>(cb) * C + c, static_cast<int64_t>(p.nblocks) * C, tA, tC, cut, meanwhile);
-  } else {
-    meanwhile();
+    const unsigned int rank = cluster_rank(), size = cluster_size();
+    for (unsigned int to = warp; to < size; to += kWarps) {   // a warp a CTA
+      if ((threadIdx.x & 31) < S::CL) {
+        put(&sm.tA[buf][rank][2 * cl], to, tA);
+        put(&sm.tH[buf][rank][2 * cl], to, tH);
+        if (cl == 0) put(&sm.tcut[buf][rank], to, tcut);
+      }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    F2 h = state;   // entering the tile
+#pragma unroll 4
+    for (unsigned int i = 0; i < size; ++i) {
+      if (i == rank) h = state;
+      state = act(sm.tcut[buf][i], load_pair(&sm.tA[buf][i][2 * cl]), load_pair(&sm.tH[buf][i][2 * cl]), state);
+    }
+    return act(bcut, bA, bH, h);
   }
-  float h = ck;
-#pragma unroll
-  for (int i = 0; i < NP; ++i)
-    if (i < part) h = act(sm.preset[i], sm.pA[i][c], sm.pH[i][c], h);
-#pragma unroll
-  for (int i = 0; i < GP; ++i) {
-    const int g = part * GP + i;
-    sm.H[g][c] = h;
-    h = act(sm.reset[g], A[i], H[i], h);
-  }
-  __syncthreads();
-  float b = sm.cin[c];
-#pragma unroll
-  for (int i = NP - 1; i >= 0; --i)
-    if (i > part) b = act(sm.cpreset[i], sm.pA[i][c], sm.pC[i][c], b);
-#pragma unroll
-  for (int i = GP - 1; i >= 0; --i) {
-    const int g = part * GP + i;
-    sm.Cc[g][c] = b;
-    b = act(sm.creset[g], A[i], Cc[i], b);
-  }
-  __syncthreads();
 }
 
-// The tiles a CTA works on, one after the other: by ticket where tiles wait for one another, so
-// that a tile is only waited for once somebody works on it (tickets are drawn ahead, but in
-// order: the holder of the smallest unfinished one works on it), else dealt out.
-__device__ __forceinline__ int next_tile(const RecArgs& p, int nth) {
-  if (p.ntiles > 1) return static_cast<int>(atomicAdd(p.ticket, 1u) + 1u);
-  return static_cast<int>(blockIdx.x + static_cast<unsigned int>(nth) * gridDim.x);
-}
-__device__ __forceinline__ void place(const RecArgs& p, int tile, Tile& t) {
-  t.k = tile / p.nblocks;
-  t.cb = tile - t.k * p.nblocks;
-}
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
-// Both walks.  Ahead of the tile being worked on, the next one's rows are on their way into shared
-// memory and the one's after it are asked for; `scout`, a thread of the last warp, draws and looks
-// up the tiles while the first warps wait for the chain.
-template <class S, bool TIED> __global__ void __launch_bounds__(kThreads, FB) rec_forward_kernel(RecArgs p) {
+template <class S, bool TIED, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
   using T = typename S::T;
-  using P = Pack<T, S::V>;
-  constexpr int V = S::V, R = S::R, U = S::U;
+  constexpr int R = S::R, L = S::L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<Smem<S, 2, 2>*>(smem_raw);
-  const int tid = threadIdx.x, cl = tid % S::CL, g = tid / S::CL;
-  const bool scout = tid == kThreads - 32;
+  auto& sm = *reinterpret_cast<Smem<S, 2>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
+  const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;   // tiles a round
+  const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
+  const bool in = c0 < p.W;
   const int64_t limit = row_limit(p);
-  const int filled = static_cast<int>((limit + S::L - 1) / S::L);   // tiles with rows, in time
+  const int filled = static_cast<int>((limit + L - 1) / L);   // tiles with rows
   rowless_sequences(p, p.s0, p.s1);
-
-  auto fetch = [&](const Tile& t, int buf) {   // a group for every call, so that they can be counted
-    if (t.k < filled) {
-      const int64_t row0 = static_cast<int64_t>(t.k) * S::L + g * R;
-      const int c0 = t.cb * S::C + cl * V;
-      const T* x = static_cast<const T*>(p.x) + row0 * p.W + c0;
-      const T* f = static_cast<const T*>(p.f) + row0 * p.W + c0;
-      if (c0 < p.W && row0 + R <= limit) {
-#pragma unroll
-        for (int i = 0; i < R; ++i, x += p.W, f += p.W) {
-          copy_async(&sm.raw[buf][0][i][tid], x, true);
-          copy_async(&sm.raw[buf][1][i][tid], f, true);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i, x += p.W, f += p.W) {
-          const bool in = c0 < p.W && row0 + i < limit;
-          copy_async(&sm.raw[buf][0][i][tid], in ? x : static_cast<const T*>(p.x), in);
-          copy_async(&sm.raw[buf][1][i][tid], in ? f : static_cast<const T*>(p.f), in);
-        }
-      }
-    }
-    copy_commit();
+  zero_columns<S, 2>(p, sm, cb * S::C);
+  __syncthreads();
+  int t = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  auto fetch = [&](int tile, int buf) {
+    if (tile < filled) fetch_rows<S, 2>(p, sm, buf, static_cast<int64_t>(tile) * L, cb * S::C, limit);
+    commit_rows();   // a group for every call, so that they can be counted
   };
-  if (scout) {
-    for (int n = 0; n < 2; ++n) {
-      place(p, next_tile(p, n), sm.tile[n]);
-      if (sm.tile[n].k < filled) look_up<S>(p, static_cast<int64_t>(sm.tile[n].k) * S::L, limit, sm.tile[n]);
-    }
+  fetch(t, 0);
+  fetch(t + stride, 1);
+  if (CLUSTER) {   // everybody's shared memory is there
+    cluster_arrive();
+    cluster_wait();
   }
-  __syncthreads();
-  Tile tile = sm.tile[0];
-  fetch(tile, 0);
-  fetch(sm.tile[1], 1);
-  if (tile.k < filled && tile.any)
-    mark_rows<S>(p, static_cast<int64_t>(tile.k) * S::L, limit, tile.seq, sm.start[0], sm.end[0]);
-  __syncthreads();
-  int slot = 0;   // n % 3
-  for (int n = 0; tile.k < filled; ++n) {
-    const int buf = n & 1, slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
-    const int64_t row0 = static_cast<int64_t>(tile.k) * S::L + g * R;
-    const int c0 = tile.cb * S::C + cl * V;
-    const bool in = c0 < p.W;
-    int drawn = 0;
-    if (scout) drawn = next_tile(p, n + 2);
-    copy_wait<1>();
+  Sequence seq{};
+  if (t < filled) seq = sequence_of(p, static_cast<int64_t>(t) * L, 0);
+  F2 state = splat(0.f);   // entering the round's first tile
+  // every CTA of a cluster goes through every round, with a tile that has rows or without
+  for (int buf = 0; t - t % stride < filled; t += stride, buf ^= 1) {
+    const int64_t r0 = static_cast<int64_t>(t) * L, row0 = r0 + g * R;
+    // without marks every row of the tile is in one sequence, and none is its first or last
+    const bool any = seq.lo >= r0 || seq.hi <= r0 + L || r0 + L > limit;
+    if (any) {
+      __syncthreads();
+      mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.start, sm.end);
+      __syncthreads();
+    }
+    auto tile = [&](auto marked) {   // the marks' tests are kept out of the common case
+    constexpr bool kMarked = decltype(marked)::value;
+    const T* x = &sm.raw[buf][0][g * R][2 * cl];
+    const T* f = &sm.raw[buf][1][g * R][2 * cl];
+    rows_here();
 
-    float2 a[R][U], b[R][U], A[U], H[U];
-    int reset = 0;
-#pragma unroll
-    for (int e = 0; e < U; ++e) { A[e] = splat(1.f); H[e] = splat(0.f); }
-    auto rows_in = [&](auto marked) {
+    F2 a[R], b[R], A = splat(1.f), H = splat(0.f);
+    int cut = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
-        if constexpr (decltype(marked)::value) {
-          const int s = sm.start[buf][g * R + i];
+        if constexpr (kMarked) {
+          const int s = sm.start[g * R + i];
           if (s >= 0) {
-            reset = 1;
-#pragma unroll
-            for (int e = 0; e < U; ++e) H[e] = splat(0.f);
-            if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
+            cut = 1;
+            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, s, c0, p.W);
           }
         }
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-          float2 keep;
-          gates<T>(fr.pair(e), a[i][e], keep);
-          b[i][e] = TIED ? mul2(keep, xr.pair(e)) : xr.pair(e);
-          H[e] = fma2(a[i][e], H[e], b[i][e]);
-          A[e] = mul2(A[e], a[i][e]);
-        }
+        F2 keep;
+        gates<T>(load_pair(f + i * S::C), a[i], keep);
+        b[i] = load_pair(x + i * S::C);
+        if (TIED) b[i] = mul2(keep, b[i]);
+        H = fma2(a[i], H, b[i]);
+        A = mul2(A, a[i]);
       }
-    };
-    if (tile.any) rows_in(Yes{}); else rows_in(No{});
-    store_f32<V>(&sm.A[g][cl * V], A);
-    store_f32<V>(&sm.H[g][cl * V], H);
-    if (cl == 0) sm.reset[g] = reset;
-    if (scout) place(p, drawn, sm.tile[slot2]);
+    __syncwarp();   // the warp's rows have been read
+    fetch(t + 2 * stride, buf);
+    F2 eA, eH;
+    int ecut;
+    compose_warp<S::CL, false>(A, H, cut, eA, eH, ecut);
+    if (lane >= 32 - S::CL) {
+      *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
+      *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
+      if (lane == 31) sm.cut[buf][warp] = cut;
+    }
     __syncthreads();
-    const Tile next = sm.tile[slot1];
-    fold_forward<S>(p, sm, tile.k, tile.cb, [&] {
-      fetch(sm.tile[slot2], buf);
-      if (next.k < filled && next.any)
-        mark_rows<S>(p, static_cast<int64_t>(next.k) * S::L, limit, next.seq, sm.start[buf ^ 1], sm.end[buf ^ 1]);
-      if (scout && sm.tile[slot2].k < filled)
-        look_up<S>(p, static_cast<int64_t>(sm.tile[slot2].k) * S::L, limit, sm.tile[slot2]);
-    });
-
-    if (in) {
-      float2 h[U];
-      load_f32<V>(&sm.H[g][cl * V], h);
-      T* out = p.out ? static_cast<T*>(p.out) + row0 * p.W + c0 : nullptr;
-      auto rows_out = [&](auto marked) {
+    F2 h = fold_warps<S, CLUSTER, false, kMarked>(sm, buf, sm.H[buf], sm.cut[buf], cl, state);
+    if (in && r0 < limit) {
+      h = act(ecut, eA, eH, h);
+      if (p.ck && row0 % kCkRows == 0 && row0 < limit) {
+        const int s = kMarked ? sm.start[g * R] : -1;
+        store_pair<S::VEC>(p.ck + row0 / kCkRows * p.W + c0, s >= 0 ? state_or_zero<S::VEC>(p.s0, s, c0, p.W) : h, c0, p.W);
+      }
+      if (p.out) {   // else the checkpoints are all that is wanted
+        // a base the whole CTA shares and 32-bit offsets from it (L * W < 2^31)
+        T* out = static_cast<T*>(p.out) + r0 * p.W + cb * S::C;
+        unsigned int at = static_cast<unsigned int>(g * R) * static_cast<unsigned int>(p.W) + 2 * cl;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if constexpr (decltype(marked)::value) {
-            if (row0 + i >= limit) break;
-            const int s = sm.start[buf][g * R + i];
-            if (s >= 0) {
-#pragma unroll
-              for (int e = 0; e < U; ++e) h[e] = splat(0.f);
-              if (p.s0) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
+          for (int i = 0; i < R; ++i, at += p.W) {
+            if constexpr (kMarked) {
+              if (row0 + i >= limit) break;
+              const int s = sm.start[g * R + i];
+              if (s >= 0) h = state_or_zero<S::VEC>(p.s0, s, c0, p.W);
+            }
+            h = fma2(a[i], h, b[i]);
+            store_pair<S::VEC>(out + at, h, c0, p.W);
+            if constexpr (kMarked) {
+              const int s = sm.end[g * R + i];
+              if (s >= 0 && p.s1) store_pair<S::VEC>(p.s1 + static_cast<int64_t>(s) * p.W + c0, h, c0, p.W);
             }
           }
-          if (i == 0 && g == 0 && p.ck) store_f32<V>(p.ck + static_cast<int64_t>(tile.k) * p.W + c0, h);
-#pragma unroll
-          for (int e = 0; e < U; ++e) h[e] = fma2(a[i][e], h[e], b[i][e]);
-          if (out) {
-            *reinterpret_cast<P*>(out) = P::from(h);
-            out += p.W;
-          }
-          if constexpr (decltype(marked)::value) {
-            const int s = sm.end[buf][g * R + i];
-            if (s >= 0 && p.s1) store_f32<V>(p.s1 + static_cast<int64_t>(s) * p.W + c0, h);
-          }
-        }
-      };
-      if (tile.any) rows_out(Yes{}); else rows_out(No{});
+      }
     }
-    tile = next;
-    slot = slot1;
+    };
+    if (any) tile(Yes{}); else tile(No{});
+    const int64_t next = r0 + static_cast<int64_t>(stride) * L;
+    if (seq.hi <= next && t + stride < filled) seq = sequence_of(p, next, p.cu ? seq.s : 0);
   }
-  copy_wait<0>();
+  if (CLUSTER) {   // nobody leaves while others may still write into its shared memory
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
-template <class S, bool TIED> __global__ void __launch_bounds__(kThreads, BB) rec_backward_kernel(RecArgs p) {
+template <class S, bool TIED, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   using T = typename S::T;
-  using P = Pack<T, S::V>;
-  constexpr int V = S::V, R = S::R, U = S::U;
+  constexpr int R = S::R, L = S::L, Q = R < 8 ? R : 8, NQ = R / Q;   // states are recomputed Q rows at a time
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<SmemBack<S, 3, 2>*>(smem_raw);
-  const int tid = threadIdx.x, cl = tid % S::CL, g = tid / S::CL;
-  const bool scout = tid == kThreads - 32;
+  auto& sm = *reinterpret_cast<SmemBack<S>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
+  const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;
+  const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
+  const bool in = c0 < p.W;
   const int64_t limit = row_limit(p);
-  const int filled = static_cast<int>((limit + S::L - 1) / S::L);
+  const int filled = static_cast<int>((limit + L - 1) / L);
   rowless_sequences(p, p.ds1, p.ds0);
-
-  auto first_row = [&](const Tile& t) { return static_cast<int64_t>(filled - 1 - t.k) * S::L; };   // back in time
-  auto fetch = [&](const Tile& t, int buf) {
-    if (t.k < filled) {
-      const int64_t row0 = first_row(t) + g * R;
-      const int c0 = t.cb * S::C + cl * V;
-      const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.f), static_cast<const T*>(p.dout)};
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const T* at = src[q] + row0 * p.W + c0;
-#pragma unroll
-        for (int i = 0; i < R; ++i, at += p.W) {
-          const bool in = c0 < p.W && row0 + i < limit;
-          copy_async(&sm.raw[buf][q][i][tid], in ? at : src[q], in);
-        }
-      }
-    }
-    copy_commit();
+  zero_columns<S, 3>(p, sm, cb * S::C);
+  __syncthreads();
+  int k = CLUSTER ? static_cast<int>(cluster_rank()) : 0;   // tiles are counted from the last
+  auto fetch = [&](int tile, int buf) {
+    if (tile < filled) fetch_rows<S, 3>(p, sm, buf, static_cast<int64_t>(filled - 1 - tile) * L, cb * S::C, limit);
+    commit_rows();
   };
-  if (scout) {
-    for (int n = 0; n < 2; ++n) {
-      place(p, next_tile(p, n), sm.tile[n]);
-      if (sm.tile[n].k < filled) look_up<S>(p, first_row(sm.tile[n]), limit, sm.tile[n]);
-    }
+  fetch(k, 0);
+  fetch(k + stride, 1);
+  if (CLUSTER) {
+    cluster_arrive();
+    cluster_wait();
   }
-  __syncthreads();
-  Tile tile = sm.tile[0];
-  fetch(tile, 0);
-  fetch(sm.tile[1], 1);
-  if (tile.k < filled && tile.any) mark_rows<S>(p, first_row(tile), limit, tile.seq, sm.start[0], sm.end[0]);
-  __syncthreads();
-  int slot = 0;   // n % 3
-  for (int n = 0; tile.k < filled; ++n) {
-    const int buf = n & 1, slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
-    const int64_t row0 = first_row(tile) + g * R;
-    const int c0 = tile.cb * S::C + cl * V;
-    const bool in = c0 < p.W;
-    int drawn = 0;
-    if (scout) drawn = next_tile(p, n + 2);
-    const int cf = tile.cb * S::C + tid % S::C;   // the thread's channel in the fold
-    const float ck = cf < p.W ? p.ck[static_cast<int64_t>(filled - 1 - tile.k) * p.W + cf] : 0.f;
-    copy_wait<1>();
+  Sequence seq{};
+  if (k < filled) seq = sequence_of(p, static_cast<int64_t>(filled - 1 - k) * L, 0);
+  F2 flow = splat(0.f);   // entering the round's first tile from behind
+  for (int buf = 0; k - k % stride < filled; k += stride, buf ^= 1) {
+    const bool rows = k < filled;   // a CTA without a tile in the last round takes part with an empty one
+    const int64_t r0 = rows ? static_cast<int64_t>(filled - 1 - k) * L : limit, row0 = r0 + g * R;
+    const bool any = seq.lo >= r0 || seq.hi <= r0 + L || r0 + L > limit;
+    if (any) {
+      __syncthreads();
+      mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.start, sm.end);
+      __syncthreads();
+    }
+    auto tile = [&](auto marked) {
+    constexpr bool kMarked = decltype(marked)::value;
+    const T* x = &sm.raw[buf][0][g * R][2 * cl];
+    const T* f = &sm.raw[buf][1][g * R][2 * cl];
+    const T* d = &sm.raw[buf][2][g * R][2 * cl];
+    F2 hin = splat(0.f);   // the state entering the tile
+    if (in && rows) hin = load_state<S::VEC>(p.ck + r0 / kCkRows * p.W + c0, c0, p.W);
+    rows_here();
 
-    // What the rows do to h, forward, and to the flow into the state before them, backward.
-    float2 a[R][U], A[U], H[U], cc[U];
-    int reset = 0, creset = 0;
-#pragma unroll
-    for (int e = 0; e < U; ++e) { A[e] = splat(1.f); H[e] = cc[e] = splat(0.f); }
-    auto rows_in = [&](auto marked) {
+    // What the group's rows do to the state, and to the flow into the state before them: C grows with
+    // each row by the row's own part, carried over the rows before it (and the row) by A.  Every Q rows,
+    // what the rows so far do to the state is kept.
+    F2 a[R], keep[R], A = splat(1.f), H = splat(0.f), C = splat(0.f), qA[NQ], qH[NQ];
+    int cut = 0, ccut = 0;
+    unsigned int qcut = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
-        if constexpr (decltype(marked)::value) {
-          const int s = sm.start[buf][g * R + i];
+        if (i % Q == 0) {
+          qA[i / Q] = A;
+          qH[i / Q] = H;
+          qcut |= static_cast<unsigned int>(cut) << (i / Q);
+        }
+        gates<T>(load_pair(f + i * S::C), a[i], keep[i]);
+        A = mul2(A, a[i]);
+        F2 v = load_pair(d + i * S::C);
+        if constexpr (kMarked) {
+          const int s = sm.start[g * R + i], e = sm.end[g * R + i];
           if (s >= 0) {
-            reset = 1;
-#pragma unroll
-            for (int e = 0; e < U; ++e) H[e] = splat(0.f);
-            if (p.s0 && in) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, H);
+            cut = 1;
+            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, s, c0, p.W);
           }
-        }
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-          float2 keep;
-          gates<T>(fr.pair(e), a[i][e], keep);
-          H[e] = fma2(a[i][e], H[e], TIED ? mul2(keep, xr.pair(e)) : xr.pair(e));
-          A[e] = mul2(A[e], a[i][e]);
-        }
-      }
-#pragma unroll
-      for (int i = R - 1; i >= 0; --i) {
-        const P dr = sm.raw[buf][2][i][tid];
-        if constexpr (decltype(marked)::value) {
-          const int s = sm.end[buf][g * R + i];
-          if (s >= 0) {
-            creset = 1;
-#pragma unroll
-            for (int e = 0; e < U; ++e) cc[e] = splat(0.f);
-            if (p.ds1 && in) load_f32<V>(p.ds1 + static_cast<int64_t>(s) * p.W + c0, cc);
+          if (!ccut) {   // rows behind the end of a sequence flow to no row before it
+            if (e >= 0) v = add2(v, state_or_zero<S::VEC>(in ? p.ds1 : nullptr, e, c0, p.W));
+            C = fma2(A, v, C);
           }
+          ccut |= e >= 0;
+        } else {
+          C = fma2(A, v, C);
         }
-#pragma unroll
-        for (int e = 0; e < U; ++e) cc[e] = mul2(a[i][e], add2(dr.pair(e), cc[e]));
+        const F2 xv = load_pair(x + i * S::C);
+        H = fma2(a[i], H, TIED ? mul2(keep[i], xv) : xv);
       }
-    };
-    if (tile.any) rows_in(Yes{}); else rows_in(No{});
-    store_f32<V>(&sm.A[g][cl * V], A);
-    store_f32<V>(&sm.H[g][cl * V], H);
-    store_f32<V>(&sm.Cc[g][cl * V], cc);
-    if (cl == 0) {
-      sm.reset[g] = reset;
-      sm.creset[g] = creset;
+    const F2 gA = A;   // the group's own
+    F2 eA = splat(1.f), eH = splat(0.f), bA, bC;
+    int ecut = 0, bcut;
+    F2 wA = gA;
+    compose_warp<S::CL, false>(wA, H, cut, eA, eH, ecut);
+    compose_warp<S::CL, true>(A, C, ccut, bA, bC, bcut);
+    if (lane < S::CL) {   // all groups, from the last
+      *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
+      *reinterpret_cast<F2*>(&sm.Cc[buf][warp][2 * cl]) = C;
+      if (lane == 0) sm.ccut[buf][warp] = ccut;
     }
-    if (scout) place(p, drawn, sm.tile[slot2]);
+    if (lane >= 32 - S::CL) {
+      *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
+      if (lane == 31) sm.cut[buf][warp] = cut;
+    }
     __syncthreads();
-    const Tile next = sm.tile[slot1];
-    fold_both<S>(p, sm, tile.k, tile.cb, ck, [&] {
-      if (next.k < filled && next.any)
-        mark_rows<S>(p, first_row(next), limit, next.seq, sm.start[buf ^ 1], sm.end[buf ^ 1]);
-      if (scout && sm.tile[slot2].k < filled) look_up<S>(p, first_row(sm.tile[slot2]), limit, sm.tile[slot2]);
-    });
-
-    if (in) {
-      float2 prev[R][U], h[U];
-      load_f32<V>(&sm.H[g][cl * V], h);
-      load_f32<V>(&sm.Cc[g][cl * V], cc);
-      const int64_t last = (row0 + R - 1) * p.W + c0;
-      T* dx = static_cast<T*>(p.dx) + last;
-      T* df = static_cast<T*>(p.df) + last;
-      auto rows_out = [&](auto marked) {
+    F2 c = fold_warps<S, CLUSTER, true, kMarked>(sm, buf, sm.Cc[buf], sm.ccut[buf], cl, flow);
+    if (in && rows) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if constexpr (decltype(marked)::value) {
-            const int s = sm.start[buf][g * R + i];
-            if (s >= 0) {
+      for (int w = 0; w < kWarps - 1; ++w)
+        if (w < warp) hin = act(kMarked ? sm.cut[buf][w] : 0, load_pair(&sm.A[buf][w][2 * cl]), load_pair(&sm.H[buf][w][2 * cl]), hin);
+      hin = act(ecut, eA, eH, hin);
+      c = act(bcut, bA, bC, c);
+      T* dx = static_cast<T*>(p.dx) + r0 * p.W + cb * S::C;
+      T* df = static_cast<T*>(p.df) + r0 * p.W + cb * S::C;
+      unsigned int at = static_cast<unsigned int>(g * R + R - 1) * static_cast<unsigned int>(p.W) + 2 * cl;
 #pragma unroll
-              for (int e = 0; e < U; ++e) h[e] = splat(0.f);
-              if (p.s0) load_f32<V>(p.s0 + static_cast<int64_t>(s) * p.W + c0, h);
+        for (int q = NQ - 1; q >= 0; --q) {
+          F2 h = act(qcut >> q & 1u, qA[q], qH[q], hin), prev[Q];
+#pragma unroll
+          for (int j = 0; j < Q; ++j) {
+            const int i = q * Q + j;
+            if constexpr (kMarked) {
+              const int s = sm.start[g * R + i];
+              if (s >= 0) h = state_or_zero<S::VEC>(p.s0, s, c0, p.W);
             }
+            const F2 xv = load_pair(x + i * S::C);
+            prev[j] = TIED ? fma2(xv, splat(-1.f), h) : h;   // what the gate weighs against the input
+            h = fma2(a[i], h, TIED ? mul2(keep[i], xv) : xv);
           }
-          const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid];
 #pragma unroll
-          for (int e = 0; e < U; ++e) {
-            prev[i][e] = h[e];
-            if (i + 1 < R) {
-              float2 again, keep;
-              if (TIED) gates<T>(fr.pair(e), again, keep);
-              h[e] = fma2(a[i][e], h[e], TIED ? mul2(keep, xr.pair(e)) : xr.pair(e));
+          for (int j = Q - 1; j >= 0; --j, at -= p.W) {
+            const int i = q * Q + j;
+            if constexpr (kMarked) {
+              if (row0 + i >= limit) continue;
+              const int s = sm.end[g * R + i];
+              if (s >= 0) c = state_or_zero<S::VEC>(p.ds1, s, c0, p.W);
+            }
+            const F2 G1 = add2(load_pair(d + i * S::C), c);
+            c = mul2(a[i], G1);
+            store_pair<S::VEC>(dx + at, TIED ? mul2(keep[i], G1) : G1, c0, p.W);
+            store_pair<S::VEC>(df + at, mul2(mul2(keep[i], c), prev[j]), c0, p.W);
+            if constexpr (kMarked) {
+              const int s = sm.start[g * R + i];
+              if (s >= 0 && p.ds0) store_pair<S::VEC>(p.ds0 + static_cast<int64_t>(s) * p.W + c0, c, c0, p.W);
             }
           }
         }
-#pragma unroll
-        for (int i = R - 1; i >= 0; --i, dx -= p.W, df -= p.W) {
-          if constexpr (decltype(marked)::value) {
-            if (row0 + i >= limit) continue;
-            const int s = sm.end[buf][g * R + i];
-            if (s >= 0) {
-#pragma unroll
-              for (int e = 0; e < U; ++e) cc[e] = splat(0.f);
-              if (p.ds1) load_f32<V>(p.ds1 + static_cast<int64_t>(s) * p.W + c0, cc);
-            }
-          }
-          const P xr = sm.raw[buf][0][i][tid], fr = sm.raw[buf][1][i][tid], dr = sm.raw[buf][2][i][tid];
-          float2 ox[U], of[U];
-#pragma unroll
-          for (int e = 0; e < U; ++e) {
-            float2 again, keep;
-            gates<T>(fr.pair(e), again, keep);
-            const float2 G1 = add2(dr.pair(e), cc[e]);
-            ox[e] = TIED ? mul2(keep, G1) : G1;
-            cc[e] = mul2(a[i][e], G1);
-            const float2 d = TIED ? fma2(xr.pair(e), splat(-1.f), prev[i][e]) : prev[i][e];
-            of[e] = mul2(mul2(keep, cc[e]), d);
-          }
-          *reinterpret_cast<P*>(dx) = P::from(ox);
-          *reinterpret_cast<P*>(df) = P::from(of);
-          if constexpr (decltype(marked)::value) {
-            const int s = sm.start[buf][g * R + i];
-            if (s >= 0 && p.ds0) store_f32<V>(p.ds0 + static_cast<int64_t>(s) * p.W + c0, cc);
-          }
-        }
-      };
-      if (tile.any) rows_out(Yes{}); else rows_out(No{});
     }
-    fetch(sm.tile[slot2], buf);   // the buffer has been read to the end
-    tile = next;
-    slot = slot1;
+    __syncwarp();   // the warp's rows have been read to the end
+    fetch(k + 2 * stride, buf);
+    };
+    if (any) tile(Yes{}); else tile(No{});
+    if (k + stride < filled) {
+      const int64_t next = r0 - static_cast<int64_t>(stride) * L;
+      if (seq.lo > next) seq = sequence_of(p, next, 0);
+    }
   }
-  copy_wait<0>();
+  if (CLUSTER) {
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 template <typename T>
@@ -867,26 +681,20 @@ __global__ void __launch_bounds__(256) rec_step_kernel(const T* __restrict__ x, 
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const float xv = load_elem<T>(x, i);
-    float2 a, keep;
-    gates<T>(make_float2(load_elem<T>(f, i), 0.f), a, keep);
-    const float h = fmaf(a.x, state[i], tied ? keep.x * xv : xv);
+    F2 a, keep;
+    gates<T>(make_f2(load_elem<T>(f, i), 0.f), a, keep);
+    const float h = fmaf(split(a).x, state[i], tied ? split(keep).x * xv : xv);
     state[i] = h;
     store_elem<T>(out, i, h);
   }
 }
 
-using ForwardB = Shape<uint16_t, FSV, FSC, FSR>;
-using BackwardB = Shape<uint16_t, BSV, BSC, BSR>;
-using VectorF = Shape<float, 4, 8, 4>;       // 128 rows x 32 channels
-using ScalarB = Shape<uint16_t, 1, 32, 16>;  // 128 rows x 32 channels
-using ScalarF = Shape<float, 1, 32, 16>;
-
 bool vectors(int W, la_dtype dt) { return W % (dt == LA_BF16 ? 8 : 4) == 0; }
 
 int sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
   return n;
 }
 
@@ -894,85 +702,94 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-template <class K> cudaError_t launch_kernel(K kernel, unsigned grid, size_t smem, const RecArgs& p, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+#ifndef MAXCL
+#define MAXCL kMaxCluster
+#endif
+#ifndef R16
+#define R16 16
+#endif
+#ifndef R32
+#define R32 8
+#endif
+#ifndef CLF
+#define CLF 16
+#endif
+#ifndef CLB
+#define CLB 16
+#endif
+template <class K>
+cudaError_t launch_kernel(K kernel, int nblocks, int cluster, size_t smem, const RecArgs& p, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(nblocks) * static_cast<unsigned>(cluster));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, p);
+}
+template <class S, bool TIED> cudaError_t launch_shape(RecArgs p, bool backward, cudaStream_t stream) {
+  p.nblocks = (p.W + S::C - 1) / S::C;
+  const int64_t tiles = (p.tokens + S::L - 1) / S::L, want = 2 * static_cast<int64_t>(sm_count());
+  int cluster = 1;   // as many CTAs as fill the GPU, no more than there are tiles
+  while (cluster < MAXCL && cluster < tiles && static_cast<int64_t>(p.nblocks) * cluster * 2 <= want) cluster *= 2;
+  if (backward)
+    return cluster > 1 ? launch_kernel(rec_backward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(SmemBack<S>), p, stream)
+                       : launch_kernel(rec_backward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(SmemBack<S>), p, stream);
+  return cluster > 1 ? launch_kernel(rec_forward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(Smem<S, 2>), p, stream)
+                     : launch_kernel(rec_forward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(Smem<S, 2>), p, stream);
+}
+template <typename T, int CL, int R> cudaError_t launch_typed(const RecArgs& p, bool vec, bool backward, cudaStream_t stream) {
+  if (vec)
+    return p.tied ? launch_shape<Shape<T, CL, R, true>, true>(p, backward, stream)
+                  : launch_shape<Shape<T, CL, R, true>, false>(p, backward, stream);
+  return p.tied ? launch_shape<Shape<T, CL, R, false>, true>(p, backward, stream)
+                : launch_shape<Shape<T, CL, R, false>, false>(p, backward, stream);
 }
 
-template <class S> cudaError_t launch_forward(RecArgs p, cudaStream_t stream) {
-  p.nblocks = (p.W + S::C - 1) / S::C;
-  const int64_t tiles = static_cast<int64_t>(p.ntiles) * p.nblocks, most = FB * static_cast<int64_t>(sm_count());
-  const unsigned grid = static_cast<unsigned>(tiles < most ? tiles : most);
-  const size_t smem = sizeof(Smem<S, 2, 2>);
-  return p.tied ? launch_kernel(rec_forward_kernel<S, true>, grid, smem, p, stream)
-                : launch_kernel(rec_forward_kernel<S, false>, grid, smem, p, stream);
-}
-template <class S> cudaError_t launch_backward(RecArgs p, cudaStream_t stream) {
-  p.nblocks = (p.W + S::C - 1) / S::C;
-  const int64_t tiles = static_cast<int64_t>(p.ntiles) * p.nblocks, most = BB * static_cast<int64_t>(sm_count());
-  const unsigned grid = static_cast<unsigned>(tiles < most ? tiles : most);
-  const size_t smem = sizeof(SmemBack<S, 3, 2>);
-  return p.tied ? launch_kernel(rec_backward_kernel<S, true>, grid, smem, p, stream)
-                : launch_kernel(rec_backward_kernel<S, false>, grid, smem, p, stream);
-}
-
-// Workspace: [error record] [ticket] [tiles' (A, H)] [states after the tiles] (these three set for
-// each walk) [a copy of the states that a call in place overwrites] [backward: checkpoints, for a
-// call that was given none].
+// Workspace: [error record] [a copy of the states that a call in place overwrites] [backward:
+// checkpoints, for a call that was given none].
 struct RecLayout {
-  int ntiles;
-  size_t ctl, agg, inc, copy, ck, total;
+  size_t copy, ck, total;
 };
-RecLayout rec_layout(int nseq, int64_t tokens, int W, la_dtype dt, bool backward) {
+RecLayout rec_layout(int nseq, int64_t tokens, int W, bool backward) {
   RecLayout l{};
-  const size_t cols = (static_cast<size_t>(W) + 63) / 64 * 64;   // whole tiles of 32 or 64 channels
-  l.ntiles = static_cast<int>((tokens + kCkRows - 1) / kCkRows);
-  const size_t cells = l.ntiles * cols;
-  const bool chain = l.ntiles > 1;
-  l.ctl = 256;
-  l.agg = chain ? up256(sizeof(uint64_t) * cells) : 0;
-  l.inc = chain ? up256(sizeof(unsigned int) * cells) : 0;
   l.copy = up256(sizeof(float) * static_cast<size_t>(nseq) * W);
   l.ck = backward ? up256(sizeof(float) * static_cast<size_t>((tokens + kCkRows - 1) / kCkRows) * W) : 0;
-  l.total = sizeof(ErrRec) + l.ctl + l.agg + l.inc + l.copy + l.ck;
+  l.total = sizeof(ErrRec) + l.copy + l.ck;
   return l;
 }
 
-// One walk over the tiles, forward or backward in time.
-cudaError_t launch_rec(RecArgs p, const RecLayout& l, la_dtype dt, bool backward, void* workspace,
+// One walk over the rows, forward or backward in time.
+cudaError_t launch_rec(RecArgs p, la_dtype dt, bool backward, void* workspace,
                        cudaStream_t stream) {
   char* base = static_cast<char*>(workspace) + sizeof(ErrRec);
-  p.ntiles = l.ntiles;
-  p.ticket = reinterpret_cast<unsigned int*>(base);
-  p.agg = reinterpret_cast<uint64_t*>(base + l.ctl);
-  p.inc = reinterpret_cast<unsigned int*>(base + l.ctl + l.agg);
-  // Where the states are updated in place, a tile may write what another still reads: from a copy.
+  // Where the states are updated in place, a thread may write what another still reads: from a copy.
   const float*& from = backward ? p.ds1 : p.s0;
-  const float* to = backward ? p.ds0 : p.s1;
+  float* to = backward ? p.ds0 : p.s1;
   const size_t bytes = sizeof(float) * static_cast<size_t>(p.nseq) * p.W;
   const uintptr_t fi = reinterpret_cast<uintptr_t>(from), ti = reinterpret_cast<uintptr_t>(to);
-  cudaError_t e = cudaSuccess;
   if (p.tokens == 0) {   // no rows: the states pass through
-    if (!to || from == to) return e;
-    float* dst = backward ? p.ds0 : p.s1;
-    return from ? cudaMemcpyAsync(dst, from, bytes, cudaMemcpyDeviceToDevice, stream)
-                : cudaMemsetAsync(dst, 0, bytes, stream);
+    if (!to || from == to) return cudaSuccess;
+    return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream) : cudaMemsetAsync(to, 0, bytes, stream);
   }
   if (from && to && fi < ti + bytes && ti < fi + bytes) {
-    float* copy = reinterpret_cast<float*>(base + l.ctl + l.agg + l.inc);
-    e = cudaMemcpyAsync(copy, from, bytes, cudaMemcpyDeviceToDevice, stream);
+    float* copy = reinterpret_cast<float*>(base);
+    const cudaError_t e = cudaMemcpyAsync(copy, from, bytes, cudaMemcpyDeviceToDevice, stream);
+    if (e != cudaSuccess) return e;
     from = copy;
   }
-  if (e == cudaSuccess && l.ntiles > 1) e = cudaMemsetAsync(p.ticket, 0xFF, l.ctl + l.agg + l.inc, stream);
-  if (e != cudaSuccess) return e;
   const bool vec = vectors(p.W, dt);
-  if (backward)
-    return dt == LA_BF16 ? (vec ? launch_backward<BackwardB>(p, stream) : launch_backward<ScalarB>(p, stream))
-                         : (vec ? launch_backward<VectorF>(p, stream) : launch_backward<ScalarF>(p, stream));
-  return dt == LA_BF16 ? (vec ? launch_forward<ForwardB>(p, stream) : launch_forward<ScalarB>(p, stream))
-                       : (vec ? launch_forward<VectorF>(p, stream) : launch_forward<ScalarF>(p, stream));
+  if (dt == LA_BF16)
+    return backward ? launch_typed<uint16_t, CLB, R16>(p, vec, true, stream) : launch_typed<uint16_t, CLF, R16>(p, vec, false, stream);
+  return backward ? launch_typed<float, 16, R32>(p, vec, true, stream) : launch_typed<float, 16, R32>(p, vec, false, stream);
 }
 
 la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspace, size_t ws_bytes, bool backward,
@@ -997,10 +814,8 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
                         static_cast<const void*>(p.ds0), static_cast<const void*>(p.ds1),
                         static_cast<const void*>(p.ck)})
     if (s && !aligned16(s)) return LA_ERR_INVALID_ARG;
-  const RecLayout l = rec_layout(p.nseq, p.tokens, p.W, dt, backward);
+  const RecLayout l = rec_layout(p.nseq, p.tokens, p.W, backward);
   if (!workspace || !aligned256(workspace) || ws_bytes < l.total) return LA_ERR_INVALID_ARG;
-  // tickets count tiles of 32 channels and are drawn two ahead by every CTA
-  if (static_cast<int64_t>(l.ntiles) * ((p.W + 31) / 32) > INT32_MAX - 65536) return LA_ERR_UNSUPPORTED;
   p.err = static_cast<ErrRec*>(workspace);
   p.tied = mode == LA_INPUT_TIED;
   cudaError_t e = cudaSuccess;
@@ -1008,9 +823,9 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
     RecArgs r = p;
     r.s1 = nullptr;
     r.ck = p.ck = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.total - l.ck);
-    e = launch_rec(r, l, dt, false, workspace, stream);
+    e = launch_rec(r, dt, false, workspace, stream);
   }
-  if (e == cudaSuccess) e = launch_rec(p, l, dt, backward, workspace, stream);
+  if (e == cudaSuccess) e = launch_rec(p, dt, backward, workspace, stream);
   if (e != cudaSuccess) return LA_ERR_CUDA;
   set_last_path(backward ? "recurrence-backward" : "recurrence");
   return LA_OK;
@@ -1112,7 +927,7 @@ la_status lightning_attn_gated_recurrence_step(const void* x, const void* f, voi
 size_t lightning_attn_gated_recurrence_workspace_size(int num_seqs, int total_tokens, int W, la_dtype dtype,
                                                       int backward) {
   if (num_seqs < 1 || total_tokens < 0 || W < 1 || (dtype != LA_F32 && dtype != LA_BF16)) return 0;
-  return la::rec_layout(num_seqs, total_tokens, W, dtype, backward != 0).total;
+  return la::rec_layout(num_seqs, total_tokens, W, backward != 0).total;
 }
 
 }  // extern "C"
