@@ -702,21 +702,6 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-#ifndef MAXCL
-#define MAXCL kMaxCluster
-#endif
-#ifndef R16
-#define R16 16
-#endif
-#ifndef R32
-#define R32 8
-#endif
-#ifndef CLF
-#define CLF 16
-#endif
-#ifndef CLB
-#define CLB 16
-#endif
 template <class K>
 cudaError_t launch_kernel(K kernel, int nblocks, int cluster, size_t smem, const RecArgs& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -735,11 +720,23 @@ cudaError_t launch_kernel(K kernel, int nblocks, int cluster, size_t smem, const
   c.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&c, kernel, p);
 }
+// CTAs that walk a block of channels together.  A tile takes an SM 1.5 us with one CTA on it and 1.3 us
+// with two; a round of a cluster takes 2.5 to 2.9 us with one CTA an SM, 3.9 us with two (bf16, 8192
+// values a tile, measured at 131072 x 1024: 788 us alone, 636, 367, 252 us in clusters of 2, 4, 8).  So
+// two CTAs an SM where three or more share a block, and no clusters where two would: 32768 x 4096 takes
+// 205 us with 128 CTAs alone and 223 us in pairs.  Clusters of 16 fit the GPU about as often as there
+// are pairs of them in its 8 groups of SMs; clusters of 9 to 14 left part of it idle.
+int cluster_for(int nblocks, int64_t tiles) {
+  const int fit = nblocks <= 14 ? 16 : 2 * sm_count() / nblocks;
+  int n = fit >= 16 ? 16 : fit > 8 ? 8 : fit;
+  if (n > tiles) n = static_cast<int>(tiles);
+  if (n > 8 && n < 16) n = 8;
+  return n < 3 ? 1 : n;
+}
 template <class S, bool TIED> cudaError_t launch_shape(RecArgs p, bool backward, cudaStream_t stream) {
   p.nblocks = (p.W + S::C - 1) / S::C;
-  const int64_t tiles = (p.tokens + S::L - 1) / S::L, want = 2 * static_cast<int64_t>(sm_count());
-  int cluster = 1;   // as many CTAs as fill the GPU, no more than there are tiles
-  while (cluster < MAXCL && cluster < tiles && static_cast<int64_t>(p.nblocks) * cluster * 2 <= want) cluster *= 2;
+  const int64_t tiles = (p.tokens + S::L - 1) / S::L;
+  const int cluster = cluster_for(p.nblocks, tiles);
   if (backward)
     return cluster > 1 ? launch_kernel(rec_backward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(SmemBack<S>), p, stream)
                        : launch_kernel(rec_backward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(SmemBack<S>), p, stream);
@@ -788,8 +785,8 @@ cudaError_t launch_rec(RecArgs p, la_dtype dt, bool backward, void* workspace,
   }
   const bool vec = vectors(p.W, dt);
   if (dt == LA_BF16)
-    return backward ? launch_typed<uint16_t, CLB, R16>(p, vec, true, stream) : launch_typed<uint16_t, CLF, R16>(p, vec, false, stream);
-  return backward ? launch_typed<float, 16, R32>(p, vec, true, stream) : launch_typed<float, 16, R32>(p, vec, false, stream);
+    return launch_typed<uint16_t, 16, 16>(p, vec, backward, stream);   // tiles of 256 rows x 32 channels
+  return launch_typed<float, 16, 8>(p, vec, backward, stream);         // 128 x 32
 }
 
 la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspace, size_t ws_bytes, bool backward,
