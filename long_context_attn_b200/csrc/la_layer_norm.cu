@@ -8,275 +8,397 @@
 // one read and its one write, so the deviations are squared after the mean is known and both
 // passes touch memory once.
 #include "la_common.cuh"
+#include "la_f32x2.cuh"
 
 namespace la {
 namespace {
 
-// One thread's V consecutive values, as loaded (16 bytes, or one element).
+// One thread's V consecutive values, as loaded (16 bytes, or one element), worked on in U pairs
+// (V == 1: the second half of the pair is 0 and stays 0).
 template <typename T, int V> struct Pack;
 template <> struct Pack<uint16_t, 8> {
   uint4 r;
-  __device__ __forceinline__ void unpack(float* o) const {
+  __device__ __forceinline__ void unpack(F2* o) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) o[i] = make_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
-  __device__ __forceinline__ void pack(const float* o) {
-    r = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+  __device__ __forceinline__ void pack(const F2* o) {
+    const float2 a = split(o[0]), b = split(o[1]), c = split(o[2]), d = split(o[3]);
+    r = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y));
   }
 };
 template <> struct Pack<float, 4> {
-  float4 r;
-  __device__ __forceinline__ void unpack(float* o) const { o[0] = r.x; o[1] = r.y; o[2] = r.z; o[3] = r.w; }
-  __device__ __forceinline__ void pack(const float* o) { r = make_float4(o[0], o[1], o[2], o[3]); }
+  ulonglong2 r;
+  __device__ __forceinline__ void unpack(F2* o) const { o[0].v = r.x; o[1].v = r.y; }
+  __device__ __forceinline__ void pack(const F2* o) { r = make_ulonglong2(o[0].v, o[1].v); }
 };
 template <> struct Pack<uint16_t, 1> {
   uint16_t r;
-  __device__ __forceinline__ void unpack(float* o) const { o[0] = bf16_bits_to_f32(r); }
-  __device__ __forceinline__ void pack(const float* o) { r = f32_to_bf16_bits(o[0]); }
+  __device__ __forceinline__ void unpack(F2* o) const { o[0] = make_f2(bf16_bits_to_f32(r), 0.f); }
+  __device__ __forceinline__ void pack(const F2* o) { r = f32_to_bf16_bits(split(o[0]).x); }
 };
 template <> struct Pack<float, 1> {
   float r;
-  __device__ __forceinline__ void unpack(float* o) const { o[0] = r; }
-  __device__ __forceinline__ void pack(const float* o) { r = o[0]; }
+  __device__ __forceinline__ void unpack(F2* o) const { o[0] = make_f2(r, 0.f); }
+  __device__ __forceinline__ void pack(const F2* o) { r = split(o[0]).x; }
 };
+constexpr int pairs(int V) { return (V + 1) / 2; }
 
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
   return *reinterpret_cast<const Pack<T, V>*>(p);
 }
-template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, const float* o) {
+template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, const F2* o) {
   Pack<T, V> k;
   k.pack(o);
   *reinterpret_cast<Pack<T, V>*>(p) = k;
 }
 // V fp32 values of the weight or bias (`fill` where there is none).
-template <int V> __device__ __forceinline__ void load_w(const float* p, int c, float fill, float* o) {
+template <int V> __device__ __forceinline__ void load_w(const float* p, int c, float fill, F2* o) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = fill;
+  for (int i = 0; i < pairs(V); ++i) o[i] = splat(fill);
   if (!p) return;
   if constexpr (V == 1) {
-    o[0] = __ldg(p + c);
+    o[0] = make_f2(__ldg(p + c), 0.f);
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
       const float4 t = __ldg(reinterpret_cast<const float4*>(p + c + i));
-      o[i] = t.x; o[i + 1] = t.y; o[i + 2] = t.z; o[i + 3] = t.w;
+      o[i / 2] = make_f2(t.x, t.y);
+      o[i / 2 + 1] = make_f2(t.z, t.w);
     }
   }
 }
 
-// Sum of two values over the G threads of a row, in every one of them, in a fixed order.
-// `red` alternates between calls, so one barrier a call is enough.
-template <int G> __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*red)[32], int& half) {
+// Sums over the G threads of a row, in every one of them, in a fixed order.  `red` alternates between
+// calls, so one barrier a call is enough.
+using Sums = float4[2][32];
+template <int G> __device__ __forceinline__ float row_sum(float a, Sums& red, int& half) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (G == 32) return a;
+  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5].x = a;
+  __syncthreads();
+  a = red[half][threadIdx.x % (G / 32)].x;   // every warp adds the warps' sums for itself
+#pragma unroll
+  for (int o = G / 64; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  half ^= 1;
+  return a;
+}
+template <int G> __device__ __forceinline__ float3 row_sum(float3 v, Sums& red, int& half) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
   }
-  if (G == 32) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5] = make_float2(a, b);
+  if (G == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5] = make_float4(v.x, v.y, v.z, 0.f);
   __syncthreads();
-  a = 0.f;
-  b = 0.f;
+  const float4 t = red[half][threadIdx.x % (G / 32)];
+  v = make_float3(t.x, t.y, t.z);
 #pragma unroll
-  for (int i = 0; i < G / 32; ++i) {
-    a += red[half][i].x;
-    b += red[half][i].y;
+  for (int o = G / 64; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
   }
   half ^= 1;
-  return make_float2(a, b);
+  return v;
+}
+__device__ __forceinline__ float both(F2 a) {
+  const float2 v = split(a);
+  return v.x + v.y;
 }
 
-// Mean and 1 / sqrt(variance + eps) of a row held in registers; v becomes v - mean.
-template <int V, int NV, int G>
-__device__ __forceinline__ float center(float (*v)[V], int W, float eps, int lane, float2 (*red)[32],
-                                        int& half) {
-  float a = 0.f;
+// How a row lies in its G threads: NV vectors of V values each; FULL: exactly.
+template <typename T_, int V_, int NV_, int G_, bool FULL_> struct Row {
+  using T = T_;
+  static constexpr int V = V_, NV = NV_, G = G_, U = pairs(V_);
+  static constexpr bool FULL = FULL_;
+  __device__ __forceinline__ static int column(int lane, int i) { return (lane + i * G) * V; }
+  __device__ __forceinline__ static bool in(int lane, int i, int W) { return FULL || column(lane, i) < W; }
+};
+
+// A row held in registers becomes its deviations from its mean; returns the sum of their squares over
+// the thread's own.
+template <class R>
+__device__ __forceinline__ float center(F2 (*v)[R::U], int W, int lane, Sums& red, int& half) {
+  F2 a = splat(0.f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < R::NV; ++i)
 #pragma unroll
-    for (int e = 0; e < V; ++e) a += v[i][e];
+    for (int e = 0; e < R::U; ++e) a = add2(a, v[i][e]);
   // divided, not multiplied by 1 / W: the mean of equal values is then that value
-  const float mean = row_sum<G>(a, 0.f, red, half).x / static_cast<float>(W);
-  float q = 0.f;
+  const float mean = row_sum<R::G>(both(a), red, half) / static_cast<float>(W);
+  const F2 minus = R::V == 1 ? make_f2(-mean, 0.f) : splat(-mean);
+  F2 q = splat(0.f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = (lane + i * G) * V < W;
+  for (int i = 0; i < R::NV; ++i) {
+    const bool in = R::in(lane, i, W);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      v[i][e] = in ? v[i][e] - mean : 0.f;
-      q = fmaf(v[i][e], v[i][e], q);
+    for (int e = 0; e < R::U; ++e) {
+      v[i][e] = add2(v[i][e], minus);
+      if (!in) v[i][e] = splat(0.f);
+      q = fma2(v[i][e], v[i][e], q);
     }
   }
-  return 1.0f / sqrtf(row_sum<G>(q, 0.f, red, half).x / static_cast<float>(W) + eps);
+  return both(q);
+}
+__device__ __forceinline__ float inverse_std(float squares, int W, float eps) {
+  return 1.0f / sqrtf(squares / static_cast<float>(W) + eps);
 }
 
-template <typename T, int V, int NV, int G, int TPB>
-__global__ void __launch_bounds__(TPB) layer_norm_kernel(const T* x, const T* residual, const float* __restrict__ w,
-                                                         const float* __restrict__ b, T* out, T* sum_out, int rows,
-                                                         int W, float eps) {
-  __shared__ float2 red[2][32];
-  const int lane = threadIdx.x % G;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / G) + threadIdx.x / G;
-  if (row >= rows) return;   // whole warps (G == 32), or no one (G == TPB)
-  int half = 0;
-  const int64_t base = row * W;
-  float v[NV][V];
+// Rows on their way into shared memory: SLOTS of them, NT tensors a row, in slots that only the
+// thread that will use them touches (no barriers).  SLOTS == 0: a row is read when it is used.
+template <class R, int TPB, int NT, int SLOTS> struct Ring {
+  using T = typename R::T;
+  using P = Pack<T, R::V>;
+  static constexpr size_t kBytes = sizeof(P) * SLOTS * NT * R::NV * TPB;
+  P* base;
+  const T* src[NT];
+  int W, lane;
+  __device__ __forceinline__ P* slot(int n, int q, int i) const { return base + ((n * NT + q) * R::NV + i) * TPB + threadIdx.x; }
+  __device__ __forceinline__ void fetch(int n, int64_t row, int64_t rows) const {
+    if constexpr (SLOTS > 0) {
+      if (row < rows) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * G) * V;
+        for (int q = 0; q < NT; ++q) {
+          const T* at = src[q] + row * W;
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[i][e] = 0.f;
-    if (c < W) load_pack<T, V>(x + base + c).unpack(v[i]);
+          for (int i = 0; i < R::NV; ++i) {
+            if (R::in(lane, i, W)) {
+              const unsigned int d = static_cast<unsigned int>(__cvta_generic_to_shared(slot(n, q, i)));
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(at + R::column(lane, i)) : "memory");
+            }
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
   }
-  if (residual) {
+  // The row fetched SLOTS calls of fetch() ago is here.
+  __device__ __forceinline__ void wait() const {
+    if constexpr (SLOTS > 0) asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS > 0 ? SLOTS - 1 : 0) : "memory");
+  }
+  __device__ __forceinline__ P get(int n, int q, int i, int64_t row) const {
+    if constexpr (SLOTS > 0) return *slot(n, q, i);
+    return load_pack<T, R::V>(src[q] + row * W + R::column(lane, i));
+  }
+};
+
+// A row in TPB / G groups of threads at a time; with SLOTS, by CTAs that stay, the next rows on their way.
+template <class R, int TPB, bool RES, int SLOTS, int BLOCKS>
+__global__ void __launch_bounds__(TPB, BLOCKS)
+layer_norm_kernel(const typename R::T* x, const typename R::T* residual, const float* __restrict__ w,
+                  const float* __restrict__ b, typename R::T* out, typename R::T* sum_out, int rows, int W, float eps) {
+  using T = typename R::T;
+  constexpr int V = R::V, NV = R::NV, U = R::U;
+  constexpr bool kHold = SLOTS > 0 && NV * V <= 16;   // the thread's weights and biases stay in registers
+  __shared__ Sums red;
+  extern __shared__ __align__(16) unsigned char ring_smem[];
+  const int lane = threadIdx.x % R::G;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (TPB / R::G);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / R::G) + threadIdx.x / R::G;
+  Ring<R, TPB, RES ? 2 : 1, SLOTS> ring;
+  ring.base = reinterpret_cast<Pack<T, V>*>(ring_smem);
+  ring.src[0] = x;
+  if (RES) ring.src[RES ? 1 : 0] = residual;
+  ring.W = W;
+  ring.lane = lane;
+#pragma unroll
+  for (int n = 0; n < SLOTS; ++n) ring.fetch(n, row + n * stride, rows);
+  F2 wh[kHold ? NV : 1][U], bh[kHold ? NV : 1][U];
+  if constexpr (kHold) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c < W) {
-        float u[V];
-        load_pack<T, V>(residual + base + c).unpack(u);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[i][e] += u[e];
+      if (R::in(lane, i, W)) {
+        load_w<V>(w, R::column(lane, i), 1.0f, wh[i]);
+        load_w<V>(b, R::column(lane, i), 0.0f, bh[i]);
       }
     }
   }
-  if (sum_out) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c < W) store_pack<T, V>(sum_out + base + c, v[i]);
-    }
-  }
-  const float r = center<V, NV, G>(v, W, eps, lane, red, half);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * G) * V;
-    if (c < W) {
-      float wv[V], bv[V];
-      load_w<V>(w, c, 1.0f, wv);
-      load_w<V>(b, c, 0.0f, bv);
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = fmaf(v[i][e] * r, wv[e], bv[e]);
-      store_pack<T, V>(out + base + c, v[i]);
-    }
-  }
-}
-
-// The CTA's rows are blockIdx.x * (TPB / G) + threadIdx.x / G, then every gridDim.x * (TPB / G)
-// further.  A thread keeps the sums of dout z and dout over its rows for its own columns;
-// the CTA's sums go to partial[blockIdx.x] as [dw: W][db: W].
-template <typename T, int V, int NV, int G, int TPB>
-__global__ void __launch_bounds__(TPB) layer_norm_backward_kernel(const T* s, const T* dout, const T* dsum,
-                                                                  const float* __restrict__ w, T* dx,
-                                                                  float* __restrict__ partial, int rows, int W,
-                                                                  float eps) {
-  __shared__ float2 red[2][32];
-  extern __shared__ float fold[];   // G == 32 with partial: [2][W]
-  const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  const float inv_w = 1.0f / static_cast<float>(W);
   int half = 0;
-  float dw[NV][V], db[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / G) + group; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * (TPB / G)) {
+  for (int n = 0; row < rows; row += stride, n = n + 1 < SLOTS ? n + 1 : 0) {   // whole warps, or the whole CTA
     const int64_t base = row * W;
-    float v[NV][V], d[NV][V];
+    ring.wait();
+    F2 v[NV][U];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = d[i][e] = 0.f;
-      if (c < W) {
-        load_pack<T, V>(s + base + c).unpack(v[i]);
-        load_pack<T, V>(dout + base + c).unpack(d[i]);
-      }
-    }
-    const float r = center<V, NV, G>(v, W, eps, lane, red, half);
-    float sg = 0.f, sgz = 0.f;
+      for (int e = 0; e < U; ++e) v[i][e] = splat(0.f);
+      if (R::in(lane, i, W)) {
+        ring.get(n, 0, i, row).unpack(v[i]);
+        if (RES) {
+          F2 u[U];
+          ring.get(n, RES ? 1 : 0, i, row).unpack(u);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c < W) {
-        float wv[V];
-        load_w<V>(w, c, 1.0f, wv);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float z = v[i][e] * r;
-          dw[i][e] = fmaf(d[i][e], z, dw[i][e]);
-          db[i][e] += d[i][e];
-          v[i][e] = z;
-          d[i][e] *= wv[e];
-          sg += d[i][e];
-          sgz = fmaf(d[i][e], z, sgz);
+          for (int e = 0; e < U; ++e) v[i][e] = add2(v[i][e], u[e]);
         }
       }
     }
-    const float2 m = row_sum<G>(sg, sgz, red, half);
-    const float mg = m.x * inv_w, mgz = m.y * inv_w;
+    ring.fetch(n, row + SLOTS * stride, rows);
+    if (sum_out) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (R::in(lane, i, W)) store_pack<T, V>(sum_out + base + R::column(lane, i), v[i]);
+    }
+    const F2 r = splat(inverse_std(row_sum<R::G>(center<R>(v, W, lane, red, half), red, half), W, eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c < W) {
-        float u[V];
+      if (R::in(lane, i, W)) {
+        F2 wv[U], bv[U];
+        if constexpr (!kHold) {
+          load_w<V>(w, R::column(lane, i), 1.0f, wv);
+          load_w<V>(b, R::column(lane, i), 0.0f, bv);
+        }
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = 0.f;
-        if (dsum) load_pack<T, V>(dsum + base + c).unpack(u);
+        for (int e = 0; e < U; ++e)
+          v[i][e] = fma2(mul2(v[i][e], r), kHold ? wh[kHold ? i : 0][e] : wv[e], kHold ? bh[kHold ? i : 0][e] : bv[e]);
+        store_pack<T, V>(out + base + R::column(lane, i), v[i]);
+      }
+    }
+  }
+}
+
+// As the forward; a thread keeps the sums of dout z and dout over its rows for its own columns, and
+// the CTA's go to partial[blockIdx.x] as [dw: W][db: W].
+template <class R, int TPB, bool SUM, int SLOTS, int BLOCKS>
+__global__ void __launch_bounds__(TPB, BLOCKS)
+layer_norm_backward_kernel(const typename R::T* s, const typename R::T* dout, const typename R::T* dsum,
+                           const float* __restrict__ w, typename R::T* dx, float* __restrict__ partial, int rows, int W,
+                           float eps) {
+  using T = typename R::T;
+  constexpr int V = R::V, NV = R::NV, U = R::U;
+  constexpr bool kHold = NV * V <= 16;
+  __shared__ Sums red;
+  extern __shared__ __align__(16) unsigned char ring_smem[];
+  const int lane = threadIdx.x % R::G, group = threadIdx.x / R::G;
+  const float inv_w = 1.0f / static_cast<float>(W);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (TPB / R::G);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / R::G) + group;
+  Ring<R, TPB, SUM ? 3 : 2, SLOTS> ring;
+  ring.base = reinterpret_cast<Pack<T, V>*>(ring_smem);
+  ring.src[0] = s;
+  ring.src[1] = dout;
+  if (SUM) ring.src[SUM ? 2 : 0] = dsum;
+  ring.W = W;
+  ring.lane = lane;
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] += r * (d[i][e] - mg - v[i][e] * mgz);
-        store_pack<T, V>(dx + base + c, u);
+  for (int n = 0; n < SLOTS; ++n) ring.fetch(n, row + n * stride, rows);
+  int half = 0;
+  F2 dw[NV][U], db[NV][U], wh[kHold ? NV : 1][U];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < U; ++e) dw[i][e] = db[i][e] = splat(0.f);
+    if constexpr (kHold) {
+      if (R::in(lane, i, W)) load_w<V>(w, R::column(lane, i), 1.0f, wh[kHold ? i : 0]);
+    }
+  }
+  for (int n = 0; row < rows; row += stride, n = n + 1 < SLOTS ? n + 1 : 0) {
+    const int64_t base = row * W;
+    ring.wait();
+    F2 v[NV][U], d[NV][U];
+    Pack<T, V> u[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < U; ++e) v[i][e] = d[i][e] = splat(0.f);
+      if (R::in(lane, i, W)) {
+        ring.get(n, 0, i, row).unpack(v[i]);
+        ring.get(n, 1, i, row).unpack(d[i]);
+        if (SUM) u[i] = ring.get(n, SUM ? 2 : 0, i, row);
+      }
+    }
+    ring.fetch(n, row + SLOTS * stride, rows);
+    // The squares' sum and the two of g are one reduction: z = dev r, so the sum of g z is r times that of g dev.
+    const float squares = center<R>(v, W, lane, red, half);
+    F2 sg = splat(0.f), sgd = splat(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (R::in(lane, i, W)) {
+        F2 wv[U];
+        if constexpr (!kHold) load_w<V>(w, R::column(lane, i), 1.0f, wv);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const F2 g = mul2(d[i][e], kHold ? wh[kHold ? i : 0][e] : wv[e]);
+          sg = add2(sg, g);
+          sgd = fma2(g, v[i][e], sgd);
+        }
+      }
+    }
+    const float3 m = row_sum<R::G>(make_float3(squares, both(sg), both(sgd)), red, half);
+    const float r = inverse_std(m.x, W, eps);
+    const F2 mg = splat(-m.y * inv_w), mgz = splat(-m.z * r * inv_w), r2 = splat(r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (R::in(lane, i, W)) {
+        F2 o[U], wv[U];
+        if constexpr (!kHold) load_w<V>(w, R::column(lane, i), 1.0f, wv);
+#pragma unroll
+        for (int e = 0; e < U; ++e) o[e] = splat(0.f);
+        if (SUM) u[i].unpack(o);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const F2 z = mul2(v[i][e], r2);
+          dw[i][e] = fma2(d[i][e], z, dw[i][e]);
+          db[i][e] = add2(db[i][e], d[i][e]);
+          const F2 g = fma2(d[i][e], kHold ? wh[kHold ? i : 0][e] : wv[e], mg);
+          o[e] = fma2(r2, fma2(z, mgz, g), o[e]);
+        }
+        store_pack<T, V>(dx + base + R::column(lane, i), o);
       }
     }
   }
   if (!partial) return;
   float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * W;
-  for (int k = 0; k < TPB / G; ++k) {   // the CTA's rows-in-parallel, one after the other
-    if (group == k) {
+  auto put = [&](float* to, bool add) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int c = (lane + i * G) * V + e;
-          if (c < W) {
-            if (G == TPB) {
-              out[c] = dw[i][e];
-              out[W + c] = db[i][e];
-            } else {
-              fold[c] = k ? fold[c] + dw[i][e] : dw[i][e];
-              fold[W + c] = k ? fold[W + c] + db[i][e] : db[i][e];
-            }
-          }
+      for (int e = 0; e < V; ++e) {
+        const int c = R::column(lane, i) + e;
+        if (c < W) {
+          const float2 a = split(dw[i][e / 2]), b = split(db[i][e / 2]);
+          to[c] = (add ? to[c] : 0.f) + (e % 2 ? a.y : a.x);
+          to[W + c] = (add ? to[W + c] : 0.f) + (e % 2 ? b.y : b.x);
         }
       }
     }
-    if (G != TPB) __syncthreads();
-  }
-  if (G != TPB)
+  };
+  if constexpr (R::G == TPB) {
+    put(out, false);
+  } else {   // the CTA's rows-in-parallel, one after the other
+    float* fold = reinterpret_cast<float*>(ring_smem);   // [2][W]; nothing is on its way any more
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int k = 0; k < TPB / R::G; ++k) {
+      __syncthreads();
+      if (group == k) put(fold, k > 0);
+    }
+    __syncthreads();
     for (int c = threadIdx.x; c < 2 * W; c += TPB) out[c] = fold[c];
+  }
 }
 
-// dw[c] and db[c]: the CTAs' partial sums, added in a fixed order: 8 threads a column, each
-// over every 8th CTA, then the 8 in turn.
-__global__ void __launch_bounds__(256) layer_norm_weight_sum_kernel(const float* __restrict__ partial, int parts,
-                                                                    int W, float* __restrict__ dw,
-                                                                    float* __restrict__ db) {
-  __shared__ float red[8][33];
+// dw[c] and db[c]: the CTAs' partial sums, added in a fixed order: 32 threads a column, each over
+// every 32nd CTA, then the 32 in turn.
+__global__ void __launch_bounds__(1024) layer_norm_weight_sum_kernel(const float* __restrict__ partial, int parts,
+                                                                     int W, float* __restrict__ dw,
+                                                                     float* __restrict__ db) {
+  __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;   // column of [dw: W][db: W]
   float a = 0.f;
-  if (c < 2 * W)
-    for (int k = ty; k < parts; k += 8) a += partial[static_cast<int64_t>(k) * 2 * W + c];
+  if (c < 2 * W) {
+#pragma unroll 8
+    for (int k = ty; k < parts; k += 32) a += __ldg(partial + static_cast<int64_t>(k) * 2 * W + c);
+  }
   red[ty][tx] = a;
   __syncthreads();
   if (ty == 0 && c < 2 * W) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) a += red[k][tx];
+    for (int k = 1; k < 32; ++k) a += red[k][tx];
     if (c < W) {
       if (dw) dw[c] = a;
     } else if (db) {
@@ -285,7 +407,22 @@ __global__ void __launch_bounds__(256) layer_norm_weight_sum_kernel(const float*
   }
 }
 
-constexpr int kMaxParts = 592;   // CTAs of the backward pass: 4 for each of 148 SMs
+#ifndef FT
+#define FT 512
+#endif
+#ifndef BT
+#define BT 512
+#endif
+#ifndef BT8
+#define BT8 1024
+#endif
+#ifndef BT12
+#define BT12 640
+#endif
+#ifndef FSTAY
+#define FSTAY 256
+#endif
+constexpr int kMaxParts = 1184;   // CTAs of the backward pass: at most 8 for each of 148 SMs
 
 struct LnArgs {
   const void *x, *residual, *dout, *dsum;
@@ -297,41 +434,104 @@ struct LnArgs {
   cudaStream_t stream;
 };
 
-template <typename T, int V, int NV, int G> cudaError_t ln_forward(const LnArgs& a) {
-  constexpr int TPB = G == 32 ? 128 : G;
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.rows) + TPB / G - 1) / (TPB / G));
-  layer_norm_kernel<T, V, NV, G, TPB><<<grid, TPB, 0, a.stream>>>(
-      static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.w, a.b, static_cast<T*>(a.out),
-      static_cast<T*>(a.sum_out), a.rows, a.W, a.eps);
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  return n;
+}
+// CTAs: one for each TPB / G rows, no more than fit at once.
+unsigned ln_grid(int rows, int per, int blocks, int most) {
+  const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
+  int64_t fit = static_cast<int64_t>(blocks) * sm_count();
+  if (fit > most) fit = most;
+  return static_cast<unsigned>(need < fit ? need : fit);
+}
+constexpr int clamp_slots(int n) { return n < 1 ? 1 : n > 4 ? 4 : n; }
+
+template <class R, bool RES> cudaError_t ln_forward(const LnArgs& a) {
+  using T = typename R::T;
+  constexpr int G = R::G, TPB = G == 32 ? 128 : G;
+  // wide rows: CTAs that stay, 512 threads an SM, their shared memory full of rows to come;
+  // narrow ones: a row a group, as many as fit
+  constexpr bool kStay = R::V > 1 && G >= FSTAY;
+  constexpr int BLOCKS = kStay ? (FT / TPB > 0 ? FT / TPB : 1) : 1;
+  constexpr int SLOTS = kStay ? clamp_slots(200 * 1024 / (BLOCKS * TPB) / 16 / ((RES ? 2 : 1) * R::NV)) : 0;
+  constexpr size_t smem = Ring<R, TPB, RES ? 2 : 1, SLOTS>::kBytes;
+  auto kernel = layer_norm_kernel<R, TPB, RES, SLOTS, BLOCKS>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int per = TPB / G;
+  const unsigned grid = kStay ? ln_grid(a.rows, per, BLOCKS, INT32_MAX) : static_cast<unsigned>((a.rows - 1) / per + 1);
+  kernel<<<grid, TPB, smem, a.stream>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.w, a.b,
+                                        static_cast<T*>(a.out), static_cast<T*>(a.sum_out), a.rows, a.W, a.eps);
   return cudaGetLastError();
 }
-template <typename T, int V, int NV, int G> cudaError_t ln_backward(const LnArgs& a) {
-  constexpr int TPB = G == 32 ? 256 : G;
-  const int64_t need = (static_cast<int64_t>(a.rows) + TPB / G - 1) / (TPB / G);
-  const int grid = static_cast<int>(need < kMaxParts ? need : kMaxParts);
-  const size_t smem = G == TPB || !a.partial ? 0 : 2 * sizeof(float) * a.W;
-  layer_norm_backward_kernel<T, V, NV, G, TPB><<<grid, TPB, smem, a.stream>>>(
-      static_cast<const T*>(a.x), static_cast<const T*>(a.dout), static_cast<const T*>(a.dsum), a.w,
-      static_cast<T*>(a.out), a.partial, a.rows, a.W, a.eps);
+template <class R, bool SUM> cudaError_t ln_backward(const LnArgs& a) {
+  using T = typename R::T;
+  constexpr int G = R::G, TPB = G == 32 ? 256 : G, per = TPB / G;
+  constexpr int THREADS = R::NV * R::V <= 8 ? BT8 : R::NV * R::V <= 12 ? BT12 : BT;   // an SM, by the registers of the sums
+  constexpr int BLOCKS = THREADS / TPB > 0 ? THREADS / TPB : 1;
+  constexpr int SLOTS = R::V == 1 ? 0 : clamp_slots(200 * 1024 / (BLOCKS * TPB) / 16 / ((SUM ? 3 : 2) * R::NV));
+  constexpr size_t ring = Ring<R, TPB, SUM ? 3 : 2, SLOTS>::kBytes;
+  const size_t fold = per == 1 ? 0 : 2 * sizeof(float) * a.W, smem = ring > fold ? ring : fold;
+  auto kernel = layer_norm_backward_kernel<R, TPB, SUM, SLOTS, BLOCKS>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned grid = ln_grid(a.rows, per, BLOCKS, kMaxParts);
+  kernel<<<grid, TPB, smem, a.stream>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.dout),
+                                        static_cast<const T*>(a.dsum), a.w, static_cast<T*>(a.out), a.partial, a.rows,
+                                        a.W, a.eps);
   if (a.partial)
-    layer_norm_weight_sum_kernel<<<(2 * a.W + 31) / 32, 256, 0, a.stream>>>(a.partial, grid, a.W, a.dw, a.db);
+    layer_norm_weight_sum_kernel<<<(2 * a.W + 31) / 32, 1024, 0, a.stream>>>(a.partial, static_cast<int>(grid), a.W, a.dw,
+                                                                            a.db);
   return cudaGetLastError();
 }
 
 // The threads that share a row and how much of it each holds, by the row's vectors.
+template <typename T, int V, int NV, int G> cudaError_t ln_fwd(const LnArgs& a) {
+  if (V > 1 && a.W == V * NV * G)
+    return a.residual ? ln_forward<Row<T, V, NV, G, V != 1>, true>(a) : ln_forward<Row<T, V, NV, G, V != 1>, false>(a);
+  return a.residual ? ln_forward<Row<T, V, NV, G, false>, true>(a) : ln_forward<Row<T, V, NV, G, false>, false>(a);
+}
+template <typename T, int V, int NV, int G> cudaError_t ln_bwd(const LnArgs& a) {
+  if (V > 1 && a.W == V * NV * G)
+    return a.dsum ? ln_backward<Row<T, V, NV, G, V != 1>, true>(a) : ln_backward<Row<T, V, NV, G, V != 1>, false>(a);
+  return a.dsum ? ln_backward<Row<T, V, NV, G, false>, true>(a) : ln_backward<Row<T, V, NV, G, false>, false>(a);
+}
 template <typename T, int V> cudaError_t ln_launch(const LnArgs& a, bool backward) {
   const int vecs = (a.W + V - 1) / V;
-#define LA_LN(NV, G) return backward ? ln_backward<T, V, NV, G>(a) : ln_forward<T, V, NV, G>(a)
-  if (vecs <= 32) LA_LN(1, 32);
-  if (vecs <= 64) LA_LN(2, 32);
-  if (vecs <= 128) LA_LN(4, 32);
-  if (vecs <= 256) LA_LN(2, 128);
-  if (vecs <= 512) LA_LN(2, 256);
-  if (vecs <= 1024) LA_LN(2, 512);
-  if (vecs <= 2048) LA_LN(4, 512);
-  if (vecs <= 4096) LA_LN(4, 1024);
-  if (V == 1) LA_LN(16, 1024);
-#undef LA_LN
+  if (!backward) {
+    if (vecs <= 32) return ln_fwd<T, V, 1, 32>(a);
+    if (vecs <= 64) return ln_fwd<T, V, 2, 32>(a);
+    if (vecs <= 128) return ln_fwd<T, V, 4, 32>(a);
+    if (vecs <= 192) return ln_fwd<T, V, 3, 64>(a);
+    if (vecs <= 256) return ln_fwd<T, V, 2, 128>(a);
+    if (vecs <= 512) return ln_fwd<T, V, 2, 256>(a);
+    if (vecs <= 1024) return ln_fwd<T, V, 2, 512>(a);
+    if (vecs <= 2048) return ln_fwd<T, V, 4, 512>(a);
+    if constexpr (V < 8) {
+      if (vecs <= 4096) return ln_fwd<T, V, 4, 1024>(a);
+    }
+    if constexpr (V == 1) return ln_fwd<T, V, 16, 1024>(a);
+  } else {
+    if (vecs <= 32) return ln_bwd<T, V, 1, 32>(a);
+    if (vecs <= 64) return ln_bwd<T, V, 1, 64>(a);
+    if (vecs <= 128) return ln_bwd<T, V, 1, 128>(a);
+    if (vecs <= 192) return ln_bwd<T, V, 3, 64>(a);
+    if (vecs <= 256) return ln_bwd<T, V, 2, 128>(a);
+    if (vecs <= 512) return ln_bwd<T, V, 2, 256>(a);
+    if (vecs <= 1024) return ln_bwd<T, V, 2, 512>(a);
+    if (vecs <= 2048) return ln_bwd<T, V, 4, 512>(a);
+    if constexpr (V < 8) {
+      if (vecs <= 4096) return ln_bwd<T, V, 4, 1024>(a);
+    }
+    if constexpr (V == 1) return ln_bwd<T, V, 16, 1024>(a);
+  }
   return cudaErrorInvalidValue;
 }
 
