@@ -415,16 +415,27 @@ def lightning_attn_state_prefix(gathered, rank, out, state0=None, stream=None):
         raise LightningAttnError(st, "lightning_attn_state_prefix")
 
 
+# The calls below are short (a decode step takes a few microseconds on the GPU), so their marshalling is
+# kept lean: plain integers for pointers, and the current stream's handle without a Stream object
+# (3 microseconds less a call).
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _check_like(ref, *ts):
     """Tensors of ref's shape and dtype, contiguous, all on the current CUDA device."""
     if not ref.is_cuda:
         raise ValueError(f"tensors must be on the current CUDA device, got {ref.device}")
-    dev = torch.cuda.current_device()
+    dev, shape, dtype = torch.cuda.current_device(), ref.shape, ref.dtype
     for t in (ref, *ts):
         if t is None:
             continue
-        if t.shape != ref.shape or t.dtype != ref.dtype:
-            raise ValueError(f"expected {ref.dtype} {tuple(ref.shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
         if t.get_device() != dev:
             raise ValueError(f"tensors must be on the current CUDA device cuda:{dev}, got {t.device}")
         if not t.is_contiguous():
@@ -480,9 +491,9 @@ def lightning_attn_gated_recurrence(x, f, out, state_in=None, state_out=None, ch
     _check_f32(dev, (B, W), state_in, state_out)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
-    st = _lib.lightning_attn_gated_recurrence(_ptr(x), _ptr(f), _ptr(out), _ptr(state_in), _ptr(state_out),
-                                              _ptr(checkpoints), B, T, W, _dtype(x), input_mode, _ptr(workspace), n,
-                                              _stream(stream))
+    st = _lib.lightning_attn_gated_recurrence(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
+                                              _addr(checkpoints), B, T, W, _dtype(x), input_mode, _addr(workspace), n,
+                                              _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_gated_recurrence")
 
@@ -496,9 +507,9 @@ def lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, state_in=None,
     _check_f32(dev, (n, W), state_in, state_out)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
-    st = _lib.lightning_attn_gated_recurrence_varlen(_ptr(x), _ptr(f), _ptr(out), _ptr(state_in), _ptr(state_out),
-                                                     _ptr(checkpoints), _ptr(cu_seqlens), n, total, W, _dtype(x),
-                                                     input_mode, _ptr(workspace), nb, _stream(stream))
+    st = _lib.lightning_attn_gated_recurrence_varlen(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
+                                                     _addr(checkpoints), _addr(cu_seqlens), n, total, W, _dtype(x),
+                                                     input_mode, _addr(workspace), nb, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_gated_recurrence_varlen")
 
@@ -508,8 +519,8 @@ def lightning_attn_gated_recurrence_step(x, f, out, state, input_mode=LA_INPUT_T
     B, W = x.shape
     dev = _check_like(x, f, out)
     _check_f32(dev, (B, W), state)
-    st = _lib.lightning_attn_gated_recurrence_step(_ptr(x), _ptr(f), _ptr(out), _ptr(state), B, W, _dtype(x),
-                                                   input_mode, _stream(stream))
+    st = _lib.lightning_attn_gated_recurrence_step(_addr(x), _addr(f), _addr(out), _addr(state), B, W, _dtype(x),
+                                                   input_mode, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_gated_recurrence_step")
 
@@ -523,10 +534,10 @@ def lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, state_in=None, 
     _check_f32(dev, (B, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
-    st = _lib.lightning_attn_gated_recurrence_backward(_ptr(x), _ptr(f), _ptr(dout), _ptr(dx), _ptr(df),
-                                                       _ptr(state_in), _ptr(dstate_out), _ptr(dstate_in),
-                                                       _ptr(checkpoints), B, T, W, _dtype(x), input_mode,
-                                                       _ptr(workspace), n, _stream(stream))
+    st = _lib.lightning_attn_gated_recurrence_backward(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
+                                                       _addr(state_in), _addr(dstate_out), _addr(dstate_in),
+                                                       _addr(checkpoints), B, T, W, _dtype(x), input_mode,
+                                                       _addr(workspace), n, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_gated_recurrence_backward")
 
@@ -542,11 +553,11 @@ def lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu_seqle
     _check_f32(dev, (n, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
-    st = _lib.lightning_attn_gated_recurrence_backward_varlen(_ptr(x), _ptr(f), _ptr(dout), _ptr(dx), _ptr(df),
-                                                              _ptr(state_in), _ptr(dstate_out), _ptr(dstate_in),
-                                                              _ptr(checkpoints), _ptr(cu_seqlens), n, total, W,
-                                                              _dtype(x), input_mode, _ptr(workspace), nb,
-                                                              _stream(stream))
+    st = _lib.lightning_attn_gated_recurrence_backward_varlen(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
+                                                              _addr(state_in), _addr(dstate_out), _addr(dstate_in),
+                                                              _addr(checkpoints), _addr(cu_seqlens), n, total, W,
+                                                              _dtype(x), input_mode, _addr(workspace), nb,
+                                                              _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_gated_recurrence_backward_varlen")
 
@@ -561,8 +572,8 @@ def lightning_attn_layer_norm(x, out, residual=None, sum_out=None, weight=None, 
     W = x.shape[-1]
     dev = _check_like(x, out, residual, sum_out)
     _check_f32(dev, (W,), weight, bias)
-    st = _lib.lightning_attn_layer_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(out), _ptr(sum_out),
-                                        x.numel() // W if W else 0, W, _dtype(x), eps, _stream(stream))
+    st = _lib.lightning_attn_layer_norm(_addr(x), _addr(residual), _addr(weight), _addr(bias), _addr(out), _addr(sum_out),
+                                        x.numel() // W if W else 0, W, _dtype(x), eps, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_layer_norm")
 
@@ -575,9 +586,9 @@ def lightning_attn_layer_norm_backward(s, dout, dx, dsum=None, weight=None, dwei
     dev = _check_like(s, dout, dx, dsum)
     _check_f32(dev, (W,), weight, dweight, dbias)
     n = _check_ws(dev, workspace)
-    st = _lib.lightning_attn_layer_norm_backward(_ptr(s), _ptr(dout), _ptr(dsum), _ptr(weight), _ptr(dx),
-                                                 _ptr(dweight), _ptr(dbias), s.numel() // W if W else 0, W, _dtype(s),
-                                                 eps, _ptr(workspace), n, _stream(stream))
+    st = _lib.lightning_attn_layer_norm_backward(_addr(s), _addr(dout), _addr(dsum), _addr(weight), _addr(dx),
+                                                 _addr(dweight), _addr(dbias), s.numel() // W if W else 0, W, _dtype(s),
+                                                 eps, _addr(workspace), n, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_layer_norm_backward")
 
