@@ -29,7 +29,7 @@ void set_last_path(const char* path);
 namespace {
 
 constexpr int kCkRows = LA_RECURRENCE_CHECKPOINT_ROWS;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16, kMaxBackCluster = 8;   // the backward's fill the shared memory of two CTAs an SM
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 struct RecArgs {
@@ -78,10 +78,10 @@ template <typename T> __device__ __forceinline__ void gates(F2 f, F2& a, F2& kee
     const float2 w = split(f);
     t = make_f2(min_nan(expf(-w.x), 0x1p126f), min_nan(expf(-w.y), 0x1p126f));
   }
-  const F2 d = add2(t, splat(1.0f));
+  const F2 d = fma2(t, splat(-1.0f), splat(-1.0f));   // -(1 + t)
   const float2 v = split(d);
-  F2 r = make_f2(rcp_approx(v.x), rcp_approx(v.y));
-  r = fma2(r, fma2(fma2(t, splat(-1.0f), splat(-1.0f)), r, splat(1.0f)), r);
+  F2 r = make_f2(rcp_approx(-v.x), rcp_approx(-v.y));
+  r = fma2(r, fma2(d, r, splat(1.0f)), r);
   keep = mul2(t, r);
   a = add2(r, splat(-0x1p-126f));
 }
@@ -128,23 +128,27 @@ template <typename T_, int CL_, int R_, bool VEC_> struct Shape {
   static_assert(L % kCkRows == 0 && kCkRows % R == 0, "a tile starts at a checkpoint, which a thread's first row may be");
 };
 
-template <class S, int NT> struct Smem {
+// MOST: CTAs of a cluster, at most (1: without the arrays that only clusters need).
+template <class S, int NT, int MOST> struct Smem {
   typename S::T raw[2][NT][S::L][S::C];   // of this tile and the next; each warp's rows are its own
   float A[2][kWarps][S::C], H[2][kWarps][S::C];
   int cut[2][kWarps];                     // whether a sequence starts in the warp's rows
-  int start[S::L], end[S::L];             // of a tile with marks: the sequence that starts (ends) at a row, or -1
-  float tA[2][kMaxCluster][S::C], tH[2][kMaxCluster][S::C];   // of the round's tiles, each put here by its CTA
-  int tcut[2][kMaxCluster];
+  int mark[3][S::L];                      // of the tile before, this one and the next: see mark_rows()
+  float tA[2][MOST][S::C], tH[2][MOST][S::C];   // of the round's tiles, each put here by its CTA
+  int tcut[2][MOST];
 };
 // The backward's: the same for what flows back, beside the states forward in the tile.
-template <class S> struct SmemBack : Smem<S, 3> {
+template <class S, int MOST> struct SmemBack : Smem<S, 3, MOST> {
   float Cc[2][kWarps][S::C];
   int ccut[2][kWarps];
 };
 
+template <class S, bool CLUSTER> using ForwardSmem = Smem<S, 2, CLUSTER ? kMaxCluster : 1>;
+template <class S, bool CLUSTER> using BackwardSmem = SmemBack<S, CLUSTER ? kMaxBackCluster : 1>;
+
 // A warp's rows of a tile into shared memory, not waited for; zeros outside the rows and channels.
-template <class S, int NT>
-__device__ __forceinline__ void fetch_rows(const RecArgs& p, Smem<S, NT>& sm, int buf, int64_t r0, int c0, int64_t limit) {
+template <class S, int NT, int MOST>
+__device__ __forceinline__ void fetch_rows(const RecArgs& p, Smem<S, NT, MOST>& sm, int buf, int64_t r0, int c0, int64_t limit) {
   using T = typename S::T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.f), static_cast<const T*>(p.dout)};
@@ -185,7 +189,7 @@ __device__ __forceinline__ void fetch_rows(const RecArgs& p, Smem<S, NT>& sm, in
 }
 // Zeros the buffers' columns outside the channels, which fetch_rows() then leaves alone (the caller's
 // barrier follows).
-template <class S, int NT> __device__ __forceinline__ void zero_columns(const RecArgs& p, Smem<S, NT>& sm, int c0) {
+template <class S, int NT, int MOST> __device__ __forceinline__ void zero_columns(const RecArgs& p, Smem<S, NT, MOST>& sm, int c0) {
   if (!S::VEC || c0 + S::C <= p.W) return;
   using T = typename S::T;
   T* raw = &sm.raw[0][0][0][0];
@@ -229,21 +233,27 @@ __device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, i
   q.hi = a < p.nseq ? __ldg(p.cu + a + 1) : p.tokens;
   return q;
 }
-// Marks the tile's rows where sequences start and end.
+// Whether the tile at r0 needs marks; without, every row of it is in one sequence, and none is that
+// sequence's first or last.  `q`: the sequence of the row r0.
+template <class S> __device__ __forceinline__ bool marked(const Sequence& q, int64_t r0, int64_t limit) {
+  return q.lo >= r0 || q.hi <= r0 + S::L || r0 + S::L > limit;
+}
+// Marks a tile's rows: 4 s where sequence s starts or ends, with bit 0 set where it starts and bit 1 where
+// it ends; -1 elsewhere.
+constexpr int kStart = 1, kEnd = 2;
 template <class S>
-__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int from, int* start, int* end) {
+__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int from, int* mark) {
   for (int i = threadIdx.x; i < S::L; i += kThreads) {
     const int64_t row = r0 + i;
-    int st = -1, en = -1;
+    int m = -1;
     if (row < limit) {
       const Sequence q = sequence_of(p, row, from);
       if (q.s < p.nseq && q.lo >= 0 && q.lo <= row && q.hi <= p.tokens) {
-        if (q.lo == row) st = q.s;
-        if (q.hi - 1 == row) en = q.s;
+        const int at = (q.lo == row ? kStart : 0) | (q.hi - 1 == row ? kEnd : 0);
+        if (at) m = q.s << 2 | at;
       }
     }
-    start[i] = st;
-    end[i] = en;
+    mark[i] = m;
   }
 }
 
@@ -381,12 +391,12 @@ __device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C],
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
-template <class S, bool TIED, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
+template <class S, bool TIED, bool CLUSTER, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p) {
   using T = typename S::T;
   constexpr int R = S::R, L = S::L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<Smem<S, 2>*>(smem_raw);
+  auto& sm = *reinterpret_cast<ForwardSmem<S, CLUSTER>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
   const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;   // tiles a round
   const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
@@ -394,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
   const int64_t limit = row_limit(p);
   const int filled = static_cast<int>((limit + L - 1) / L);   // tiles with rows
   rowless_sequences(p, p.s0, p.s1);
-  zero_columns<S, 2>(p, sm, cb * S::C);
+  zero_columns(p, sm, cb * S::C);
   __syncthreads();
   int t = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
   auto fetch = [&](int tile, int buf) {
-    if (tile < filled) fetch_rows<S, 2>(p, sm, buf, static_cast<int64_t>(tile) * L, cb * S::C, limit);
+    if (tile < filled) fetch_rows(p, sm, buf, static_cast<int64_t>(tile) * L, cb * S::C, limit);
     commit_rows();   // a group for every call, so that they can be counted
   };
   fetch(t, 0);
@@ -408,20 +418,34 @@ __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
     cluster_wait();
   }
   Sequence seq{};
-  if (t < filled) seq = sequence_of(p, static_cast<int64_t>(t) * L, 0);
+  bool any = true;   // whether the tile has marks
+  if (t < filled) {
+    seq = sequence_of(p, static_cast<int64_t>(t) * L, 0);
+    any = marked<S>(seq, static_cast<int64_t>(t) * L, limit);
+    if (any) mark_rows<S>(p, static_cast<int64_t>(t) * L, limit, p.cu ? seq.s : 0, sm.mark[0]);
+  } else {
+    for (int i = tid; i < L; i += kThreads) sm.mark[0][i] = -1;
+  }
+  __syncthreads();
   F2 state = splat(0.f);   // entering the round's first tile
   // every CTA of a cluster goes through every round, with a tile that has rows or without
-  for (int buf = 0; t - t % stride < filled; t += stride, buf ^= 1) {
+  for (int buf = 0, slot = 0; t - t % stride < filled; t += stride, buf ^= 1) {
     const int64_t r0 = static_cast<int64_t>(t) * L, row0 = r0 + g * R;
-    // without marks every row of the tile is in one sequence, and none is its first or last
-    const bool any = seq.lo >= r0 || seq.hi <= r0 + L || r0 + L > limit;
-    if (any) {
-      __syncthreads();
-      mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.start, sm.end);
-      __syncthreads();
+    const int* mark = sm.mark[slot] + g * R;
+    slot = slot == 2 ? 0 : slot + 1;
+    const bool now = any;
+    // the next tile's marks, before the barrier; nobody reads those of the tile before the last any more
+    if (t + stride < filled) {
+      const int64_t next = r0 + static_cast<int64_t>(stride) * L;
+      if (seq.hi <= next) seq = sequence_of(p, next, p.cu ? seq.s : 0);
+      any = marked<S>(seq, next, limit);
+      if (any) mark_rows<S>(p, next, limit, p.cu ? seq.s : 0, sm.mark[slot]);
+    } else {
+      any = true;   // a round without a tile
+      for (int i = tid; i < L; i += kThreads) sm.mark[slot][i] = -1;
     }
-    auto tile = [&](auto marked) {   // the marks' tests are kept out of the common case
-    constexpr bool kMarked = decltype(marked)::value;
+    auto tile = [&](auto with_marks) {   // the marks' tests are kept out of the common case
+    constexpr bool kMarked = decltype(with_marks)::value;
     const T* x = &sm.raw[buf][0][g * R][2 * cl];
     const T* f = &sm.raw[buf][1][g * R][2 * cl];
     rows_here();
@@ -431,10 +455,10 @@ __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if constexpr (kMarked) {
-          const int s = sm.start[g * R + i];
-          if (s >= 0) {
+          const int m = mark[i];
+          if (m >= 0 && (m & kStart)) {
             cut = 1;
-            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, s, c0, p.W);
+            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, m >> 2, c0, p.W);
           }
         }
         F2 keep;
@@ -459,8 +483,9 @@ __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
     if (in && r0 < limit) {
       h = act(ecut, eA, eH, h);
       if (p.ck && row0 % kCkRows == 0 && row0 < limit) {
-        const int s = kMarked ? sm.start[g * R] : -1;
-        store_pair<S::VEC>(p.ck + row0 / kCkRows * p.W + c0, s >= 0 ? state_or_zero<S::VEC>(p.s0, s, c0, p.W) : h, c0, p.W);
+        const int m = kMarked ? mark[0] : -1;
+        const bool first = m >= 0 && (m & kStart);
+        store_pair<S::VEC>(p.ck + row0 / kCkRows * p.W + c0, first ? state_or_zero<S::VEC>(p.s0, m >> 2, c0, p.W) : h, c0, p.W);
       }
       if (p.out) {   // else the checkpoints are all that is wanted
         // a base the whole CTA shares and 32-bit offsets from it (L * W < 2^31)
@@ -470,22 +495,20 @@ __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(RecArgs p) {
           for (int i = 0; i < R; ++i, at += p.W) {
             if constexpr (kMarked) {
               if (row0 + i >= limit) break;
-              const int s = sm.start[g * R + i];
-              if (s >= 0) h = state_or_zero<S::VEC>(p.s0, s, c0, p.W);
+              const int m = mark[i];
+              if (m >= 0 && (m & kStart)) h = state_or_zero<S::VEC>(p.s0, m >> 2, c0, p.W);
             }
             h = fma2(a[i], h, b[i]);
             store_pair<S::VEC>(out + at, h, c0, p.W);
             if constexpr (kMarked) {
-              const int s = sm.end[g * R + i];
-              if (s >= 0 && p.s1) store_pair<S::VEC>(p.s1 + static_cast<int64_t>(s) * p.W + c0, h, c0, p.W);
+              const int m = mark[i];
+              if (m >= 0 && (m & kEnd) && p.s1) store_pair<S::VEC>(p.s1 + static_cast<int64_t>(m >> 2) * p.W + c0, h, c0, p.W);
             }
           }
       }
     }
     };
-    if (any) tile(Yes{}); else tile(No{});
-    const int64_t next = r0 + static_cast<int64_t>(stride) * L;
-    if (seq.hi <= next && t + stride < filled) seq = sequence_of(p, next, p.cu ? seq.s : 0);
+    if (now) tile(Yes{}); else tile(No{});
   }
   if (CLUSTER) {   // nobody leaves while others may still write into its shared memory
     cluster_arrive();
@@ -498,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   using T = typename S::T;
   constexpr int R = S::R, L = S::L, Q = R < 8 ? R : 8, NQ = R / Q;   // states are recomputed Q rows at a time
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<SmemBack<S>*>(smem_raw);
+  auto& sm = *reinterpret_cast<BackwardSmem<S, CLUSTER>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
   const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;
   const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
@@ -506,11 +529,11 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   const int64_t limit = row_limit(p);
   const int filled = static_cast<int>((limit + L - 1) / L);
   rowless_sequences(p, p.ds1, p.ds0);
-  zero_columns<S, 3>(p, sm, cb * S::C);
+  zero_columns(p, sm, cb * S::C);
   __syncthreads();
   int k = CLUSTER ? static_cast<int>(cluster_rank()) : 0;   // tiles are counted from the last
   auto fetch = [&](int tile, int buf) {
-    if (tile < filled) fetch_rows<S, 3>(p, sm, buf, static_cast<int64_t>(filled - 1 - tile) * L, cb * S::C, limit);
+    if (tile < filled) fetch_rows(p, sm, buf, static_cast<int64_t>(filled - 1 - tile) * L, cb * S::C, limit);
     commit_rows();
   };
   fetch(k, 0);
@@ -520,19 +543,34 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     cluster_wait();
   }
   Sequence seq{};
-  if (k < filled) seq = sequence_of(p, static_cast<int64_t>(filled - 1 - k) * L, 0);
+  bool any = true;
+  if (k < filled) {
+    const int64_t r0 = static_cast<int64_t>(filled - 1 - k) * L;
+    seq = sequence_of(p, r0, 0);
+    any = marked<S>(seq, r0, limit);
+    if (any) mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.mark[0]);
+  } else {
+    for (int i = tid; i < L; i += kThreads) sm.mark[0][i] = -1;
+  }
+  __syncthreads();
   F2 flow = splat(0.f);   // entering the round's first tile from behind
-  for (int buf = 0; k - k % stride < filled; k += stride, buf ^= 1) {
+  for (int buf = 0, slot = 0; k - k % stride < filled; k += stride, buf ^= 1) {
     const bool rows = k < filled;   // a CTA without a tile in the last round takes part with an empty one
     const int64_t r0 = rows ? static_cast<int64_t>(filled - 1 - k) * L : limit, row0 = r0 + g * R;
-    const bool any = seq.lo >= r0 || seq.hi <= r0 + L || r0 + L > limit;
-    if (any) {
-      __syncthreads();
-      mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.start, sm.end);
-      __syncthreads();
+    const int* mark = sm.mark[slot] + g * R;
+    slot = slot == 2 ? 0 : slot + 1;
+    const bool now = any;
+    if (k + stride < filled) {   // the next tile's marks
+      const int64_t next = r0 - static_cast<int64_t>(stride) * L;
+      if (seq.lo > next) seq = sequence_of(p, next, 0);
+      any = marked<S>(seq, next, limit);
+      if (any) mark_rows<S>(p, next, limit, p.cu ? seq.s : 0, sm.mark[slot]);
+    } else {
+      any = true;
+      for (int i = tid; i < L; i += kThreads) sm.mark[slot][i] = -1;
     }
-    auto tile = [&](auto marked) {
-    constexpr bool kMarked = decltype(marked)::value;
+    auto tile = [&](auto with_marks) {
+    constexpr bool kMarked = decltype(with_marks)::value;
     const T* x = &sm.raw[buf][0][g * R][2 * cl];
     const T* f = &sm.raw[buf][1][g * R][2 * cl];
     const T* d = &sm.raw[buf][2][g * R][2 * cl];
@@ -557,16 +595,17 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
         A = mul2(A, a[i]);
         F2 v = load_pair(d + i * S::C);
         if constexpr (kMarked) {
-          const int s = sm.start[g * R + i], e = sm.end[g * R + i];
-          if (s >= 0) {
+          const int m = mark[i];
+          const bool starts = m >= 0 && (m & kStart), ends = m >= 0 && (m & kEnd);
+          if (starts) {
             cut = 1;
-            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, s, c0, p.W);
+            H = state_or_zero<S::VEC>(in ? p.s0 : nullptr, m >> 2, c0, p.W);
           }
           if (!ccut) {   // rows behind the end of a sequence flow to no row before it
-            if (e >= 0) v = add2(v, state_or_zero<S::VEC>(in ? p.ds1 : nullptr, e, c0, p.W));
+            if (ends) v = add2(v, state_or_zero<S::VEC>(in ? p.ds1 : nullptr, m >> 2, c0, p.W));
             C = fma2(A, v, C);
           }
-          ccut |= e >= 0;
+          ccut |= ends;
         } else {
           C = fma2(A, v, C);
         }
@@ -606,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
           for (int j = 0; j < Q; ++j) {
             const int i = q * Q + j;
             if constexpr (kMarked) {
-              const int s = sm.start[g * R + i];
-              if (s >= 0) h = state_or_zero<S::VEC>(p.s0, s, c0, p.W);
+              const int m = mark[i];
+              if (m >= 0 && (m & kStart)) h = state_or_zero<S::VEC>(p.s0, m >> 2, c0, p.W);
             }
             const F2 xv = load_pair(x + i * S::C);
             prev[j] = TIED ? fma2(xv, splat(-1.f), h) : h;   // what the gate weighs against the input
@@ -618,16 +657,16 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
             const int i = q * Q + j;
             if constexpr (kMarked) {
               if (row0 + i >= limit) continue;
-              const int s = sm.end[g * R + i];
-              if (s >= 0) c = state_or_zero<S::VEC>(p.ds1, s, c0, p.W);
+              const int m = mark[i];
+              if (m >= 0 && (m & kEnd)) c = state_or_zero<S::VEC>(p.ds1, m >> 2, c0, p.W);
             }
             const F2 G1 = add2(load_pair(d + i * S::C), c);
             c = mul2(a[i], G1);
             store_pair<S::VEC>(dx + at, TIED ? mul2(keep[i], G1) : G1, c0, p.W);
             store_pair<S::VEC>(df + at, mul2(mul2(keep[i], c), prev[j]), c0, p.W);
             if constexpr (kMarked) {
-              const int s = sm.start[g * R + i];
-              if (s >= 0 && p.ds0) store_pair<S::VEC>(p.ds0 + static_cast<int64_t>(s) * p.W + c0, c, c0, p.W);
+              const int m = mark[i];
+              if (m >= 0 && (m & kStart) && p.ds0) store_pair<S::VEC>(p.ds0 + static_cast<int64_t>(m >> 2) * p.W + c0, c, c0, p.W);
             }
           }
         }
@@ -635,11 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     __syncwarp();   // the warp's rows have been read to the end
     fetch(k + 2 * stride, buf);
     };
-    if (any) tile(Yes{}); else tile(No{});
-    if (k + stride < filled) {
-      const int64_t next = r0 - static_cast<int64_t>(stride) * L;
-      if (seq.lo > next) seq = sequence_of(p, next, 0);
-    }
+    if (now) tile(Yes{}); else tile(No{});
   }
   if (CLUSTER) {
     cluster_arrive();
@@ -647,19 +682,68 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   }
 }
 
-template <typename T>
+// One token: 14 bytes an element in bf16 (x, f, out, and the fp32 state both ways), nothing else to wait
+// for: V elements a thread, as many threads as that takes.
+template <typename T, int V>
 __global__ void __launch_bounds__(256) rec_step_kernel(const T* __restrict__ x, const T* __restrict__ f,
                                                        T* __restrict__ out, float* __restrict__ state, int64_t n,
                                                        int tied) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const float xv = load_elem<T>(x, i);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V;
+  if (i >= n) return;
+  if constexpr (V == 1) {
     F2 a, keep;
     gates<T>(make_f2(load_elem<T>(f, i), 0.f), a, keep);
+    const float xv = load_elem<T>(x, i);
     const float h = fmaf(split(a).x, state[i], tied ? split(keep).x * xv : xv);
     state[i] = h;
     store_elem<T>(out, i, h);
+  } else {
+    F2 h[V / 2], fv[V / 2], xv[V / 2];
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(state + i + e);
+      h[e / 2] = make_f2(t.x, t.y);
+      h[e / 2 + 1] = make_f2(t.z, t.w);
+    }
+    if constexpr (sizeof(T) == 2) {
+      const uint4 fr = *reinterpret_cast<const uint4*>(f + i), xr = *reinterpret_cast<const uint4*>(x + i);
+      const uint32_t fw[4] = {fr.x, fr.y, fr.z, fr.w}, xw[4] = {xr.x, xr.y, xr.z, xr.w};
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        fv[e] = make_f2(__uint_as_float(fw[e] << 16), __uint_as_float(fw[e] & 0xFFFF0000u));
+        xv[e] = make_f2(__uint_as_float(xw[e] << 16), __uint_as_float(xw[e] & 0xFFFF0000u));
+      }
+    } else {
+      const float4 fr = *reinterpret_cast<const float4*>(f + i), xr = *reinterpret_cast<const float4*>(x + i);
+      fv[0] = make_f2(fr.x, fr.y);
+      fv[1] = make_f2(fr.z, fr.w);
+      xv[0] = make_f2(xr.x, xr.y);
+      xv[1] = make_f2(xr.z, xr.w);
+    }
+    float2 o[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      F2 a, keep;
+      gates<T>(fv[e], a, keep);
+      o[e] = split(fma2(a, h[e], tied ? mul2(keep, xv[e]) : xv[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+      *reinterpret_cast<float4*>(state + i + e) = make_float4(o[e / 2].x, o[e / 2].y, o[e / 2 + 1].x, o[e / 2 + 1].y);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint4*>(out + i) = make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
+                                                      pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
+    else
+      *reinterpret_cast<float4*>(out + i) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
   }
+}
+template <typename T, int V>
+cudaError_t launch_step(const void* x, const void* f, void* out, float* state, int64_t n, int tied, cudaStream_t stream) {
+  const int64_t blocks = (n / V + 255) / 256;   // V divides n
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  rec_step_kernel<T, V><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(static_cast<const T*>(x), static_cast<const T*>(f),
+                                                                         static_cast<T*>(out), state, n, tied);
+  return cudaGetLastError();
 }
 
 bool vectors(int W, la_dtype dt) { return W % (dt == LA_BF16 ? 8 : 4) == 0; }
@@ -693,35 +777,50 @@ cudaError_t launch_kernel(K kernel, int nblocks, int cluster, size_t smem, const
   c.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&c, kernel, p);
 }
-// CTAs that walk a block of channels together.  A tile takes an SM 1.5 us with one CTA on it and 1.3 us
-// with two; a round of a cluster takes 2.5 to 2.9 us with one CTA an SM, 3.9 us with two (bf16, 8192
-// values a tile, measured at 131072 x 1024: 788 us alone, 636, 367, 252 us in clusters of 2, 4, 8).  So
-// two CTAs an SM where three or more share a block, and no clusters where two would: 32768 x 4096 takes
-// 205 us with 128 CTAs alone and 223 us in pairs.  Clusters of 16 fit the GPU about as often as there
-// are pairs of them in its 8 groups of SMs; clusters of 9 to 14 left part of it idle.
-int cluster_for(int nblocks, int64_t tiles) {
-  const int fit = nblocks <= 14 ? 16 : 2 * sm_count() / nblocks;
+// CTAs that walk a block of channels together, `blocks` of them fitting an SM.  A tile takes an SM
+// 1.5 us with one CTA on it and 1.3 us with two; a round of a cluster takes 2.5 to 2.9 us with one CTA an
+// SM, 3.9 us with two (bf16, 8192 values a tile, measured at 131072 x 1024: 788 us alone, 636, 367, 252
+// us in clusters of 2, 4, 8).  So clusters of three or more, and none where two would fit: 32768 x 4096
+// takes 205 us with 128 CTAs alone and 223 us in pairs.  A cluster lies in one group of SMs: 16 where
+// there are few enough of them; sizes of 9 to 15 left part of the GPU idle (131072 x 1024: 374 us with 9).
+int cluster_for(int nblocks, int64_t tiles, int blocks, int most) {
+  int fit = nblocks <= 14 ? 16 : blocks * sm_count() / nblocks;
+  if (fit > most) fit = most;
   int n = fit >= 16 ? 16 : fit > 8 ? 8 : fit;
   if (n > tiles) n = static_cast<int>(tiles);
   if (n > 8 && n < 16) n = 8;
   return n < 3 ? 1 : n;
 }
-template <class S, bool TIED> cudaError_t launch_shape(RecArgs p, bool backward, cudaStream_t stream) {
+template <class S, bool TIED, int BLOCKS> cudaError_t launch_forward(RecArgs p, cudaStream_t stream) {
   p.nblocks = (p.W + S::C - 1) / S::C;
-  const int64_t tiles = (p.tokens + S::L - 1) / S::L;
-  const int cluster = cluster_for(p.nblocks, tiles);
-  if (backward)
-    return cluster > 1 ? launch_kernel(rec_backward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(SmemBack<S>), p, stream)
-                       : launch_kernel(rec_backward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(SmemBack<S>), p, stream);
-  return cluster > 1 ? launch_kernel(rec_forward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(Smem<S, 2>), p, stream)
-                     : launch_kernel(rec_forward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(Smem<S, 2>), p, stream);
+  const int cluster = cluster_for(p.nblocks, (p.tokens + S::L - 1) / S::L, BLOCKS, kMaxCluster);
+  return cluster > 1 ? launch_kernel(rec_forward_kernel<S, TIED, true, BLOCKS>, p.nblocks, cluster, sizeof(ForwardSmem<S, true>), p, stream)
+                     : launch_kernel(rec_forward_kernel<S, TIED, false, BLOCKS>, p.nblocks, 1, sizeof(ForwardSmem<S, false>), p, stream);
 }
-template <typename T, int CL, int R> cudaError_t launch_typed(const RecArgs& p, bool vec, bool backward, cudaStream_t stream) {
-  if (vec)
-    return p.tied ? launch_shape<Shape<T, CL, R, true>, true>(p, backward, stream)
-                  : launch_shape<Shape<T, CL, R, true>, false>(p, backward, stream);
-  return p.tied ? launch_shape<Shape<T, CL, R, false>, true>(p, backward, stream)
-                : launch_shape<Shape<T, CL, R, false>, false>(p, backward, stream);
+template <class S, bool TIED> cudaError_t launch_backward(RecArgs p, cudaStream_t stream) {
+  p.nblocks = (p.W + S::C - 1) / S::C;
+  static_assert(sizeof(BackwardSmem<S, true>) <= 113 * 1024, "two CTAs an SM");
+  const int cluster = cluster_for(p.nblocks, (p.tokens + S::L - 1) / S::L, 2, kMaxBackCluster);
+  return cluster > 1 ? launch_kernel(rec_backward_kernel<S, TIED, true>, p.nblocks, cluster, sizeof(BackwardSmem<S, true>), p, stream)
+                     : launch_kernel(rec_backward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(BackwardSmem<S, false>), p, stream);
+}
+// bf16: tiles of 256 rows x 32 channels, 16 rows a thread; fp32, whose rows are twice the bytes: 128 x 32, 8
+// rows a thread.  The fp32 forward in clusters takes 256 x 16, so that three CTAs fit an SM and there are
+// more blocks to share (65536 x 768: 154 us against 204; the backward, 319 against 262, does not).
+template <typename T, bool VEC, bool TIED> cudaError_t launch_typed(const RecArgs& p, bool backward, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2) {
+    using S = Shape<T, 16, 16, VEC>;
+    return backward ? launch_backward<S, TIED>(p, stream) : launch_forward<S, TIED, 2>(p, stream);
+  } else {
+    using S = Shape<T, 16, 8, VEC>;
+    if (backward) return launch_backward<S, TIED>(p, stream);
+    if (cluster_for((p.W + 31) / 32, p.tokens, 2, kMaxCluster) > 1) return launch_forward<Shape<T, 8, 8, VEC>, TIED, 3>(p, stream);
+    return launch_forward<S, TIED, 2>(p, stream);
+  }
+}
+template <typename T> cudaError_t launch_walk(const RecArgs& p, bool vec, bool backward, cudaStream_t stream) {
+  if (vec) return p.tied ? launch_typed<T, true, true>(p, backward, stream) : launch_typed<T, true, false>(p, backward, stream);
+  return p.tied ? launch_typed<T, false, true>(p, backward, stream) : launch_typed<T, false, false>(p, backward, stream);
 }
 
 // Workspace: [error record] [a copy of the states that a call in place overwrites] [backward:
@@ -757,16 +856,14 @@ cudaError_t launch_rec(RecArgs p, la_dtype dt, bool backward, void* workspace,
     from = copy;
   }
   const bool vec = vectors(p.W, dt);
-  if (dt == LA_BF16)
-    return launch_typed<uint16_t, 16, 16>(p, vec, backward, stream);   // tiles of 256 rows x 32 channels
-  return launch_typed<float, 16, 8>(p, vec, backward, stream);         // 128 x 32
+  return dt == LA_BF16 ? launch_walk<uint16_t>(p, vec, backward, stream) : launch_walk<float>(p, vec, backward, stream);
 }
 
 la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspace, size_t ws_bytes, bool backward,
                      cudaStream_t stream) {
   if ((dt != LA_F32 && dt != LA_BF16) || (mode != LA_INPUT_PLAIN && mode != LA_INPUT_TIED)) return LA_ERR_INVALID_ARG;
   if (p.nseq < 1 || p.W < 1 || p.tokens < 0) return LA_ERR_INVALID_ARG;
-  if (p.tokens > INT32_MAX) return LA_ERR_UNSUPPORTED;
+  if (p.tokens > INT32_MAX || p.nseq > (1 << 28)) return LA_ERR_UNSUPPORTED;   // marks hold a sequence and two bits
   if (p.tokens > 0) {
     const void* in[3] = {p.x, p.f, p.dout};
     void* out[2] = {backward ? p.dx : p.out, p.df};
@@ -877,19 +974,17 @@ la_status lightning_attn_gated_recurrence_step(const void* x, const void* f, voi
   for (const void* t : {x, f, static_cast<const void*>(out), static_cast<const void*>(state)})
     if (!t || !la::aligned16(t)) return LA_ERR_INVALID_ARG;
   if (out == x || out == f) return LA_ERR_INVALID_ARG;
+  // the elements are independent: whole 16-byte vectors of the flat array where it is made of them
   const int64_t n = static_cast<int64_t>(B) * W;
-  const int64_t blocks = (n + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(blocks < 65535 ? blocks : 65535);
+  if (n > (int64_t(1) << 38)) return LA_ERR_UNSUPPORTED;
   const int tied = input_mode == LA_INPUT_TIED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == LA_BF16)
-    la::rec_step_kernel<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x),
-                                                        static_cast<const uint16_t*>(f),
-                                                        static_cast<uint16_t*>(out), state, n, tied);
-  else
-    la::rec_step_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(x), static_cast<const float*>(f),
-                                                     static_cast<float*>(out), state, n, tied);
-  if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+  const cudaError_t e =
+      dtype == LA_BF16 ? (n % 8 == 0 ? la::launch_step<uint16_t, 8>(x, f, out, state, n, tied, st)
+                                     : la::launch_step<uint16_t, 1>(x, f, out, state, n, tied, st))
+                       : (n % 4 == 0 ? la::launch_step<float, 4>(x, f, out, state, n, tied, st)
+                                     : la::launch_step<float, 1>(x, f, out, state, n, tied, st));
+  if (e != cudaSuccess) return LA_ERR_CUDA;
   la::set_last_path("recurrence-step");
   return LA_OK;
 }
