@@ -12,9 +12,10 @@
 // their own.
 //
 // Where the channels are too few to fill the GPU, a cluster of up to 16 CTAs walks them together,
-// each CTA a tile of the round's.  The CTAs put the (A, H) of their tiles into one another's shared
-// memory and meet at the cluster's barrier; then every thread folds the round's tiles as it folds
-// the warps.  No CTA waits for another in any other way, and the result is the same in every run.
+// each CTA a tile of the round's.  The CTAs send the (A, H) of their tiles into one another's shared
+// memory, where an mbarrier counts them; then every thread folds the round's tiles as it folds the
+// warps.  A cluster's CTAs run at the same time, so every round arrives (the wait is bounded all the
+// same), and the result is the same in every run.
 //
 // The backward walks time in reverse: with c_t = a_t (dout_t + c_{t+1}) what flows into the
 // state before row t, rows act on the c that enters them from behind as c -> A c + C with the same
@@ -134,8 +135,9 @@ template <class S, int NT, int MOST> struct Smem {
   float A[2][kWarps][S::C], H[2][kWarps][S::C];
   int cut[2][kWarps];                     // whether a sequence starts in the warp's rows
   int mark[3][S::L];                      // of the tile before, this one and the next: see mark_rows()
-  float tA[2][MOST][S::C], tH[2][MOST][S::C];   // of the round's tiles, each put here by its CTA
-  int tcut[2][MOST];
+  ulonglong2 round[2][MOST][S::CL];       // (A, H) of the round's tiles, each sent here by its CTA
+  int round_cut[2][MOST];
+  uint64_t arrived[2];                    // mbarriers: all of a round is here
 };
 // The backward's: the same for what flows back, beside the states forward in the tile.
 template <class S, int MOST> struct SmemBack : Smem<S, 3, MOST> {
@@ -325,25 +327,64 @@ __device__ __forceinline__ unsigned int cluster_size() {
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
   return n;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores into the shared memory of CTA `rank` at the place that `p` is of this one.
-__device__ __forceinline__ unsigned int there(const void* p, unsigned int rank) {
+// Only at a kernel's begin and end: its release waits for the global stores on their way.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned int shared_address(const void* p) {
+  return static_cast<unsigned int>(__cvta_generic_to_shared(p));
+}
+// The place in the shared memory of CTA `rank` that `p` is in this one's.
+__device__ __forceinline__ unsigned int at_rank(const void* p, unsigned int rank) {
   unsigned int r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<unsigned int>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(shared_address(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void put(const float* p, unsigned int rank, F2 v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(there(p, rank)), "l"(v.v) : "memory");
+// Stores into another CTA's shared memory that its mbarrier counts when they are there.
+__device__ __forceinline__ void send(unsigned int to, F2 a, F2 b, unsigned int mbar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(to), "l"(a.v),
+               "l"(b.v), "r"(mbar) : "memory");
 }
-__device__ __forceinline__ void put(const int* p, unsigned int rank, int v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there(p, rank)), "r"(v) : "memory");
+__device__ __forceinline__ void send(unsigned int to, int v, unsigned int mbar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(mbar)
+               : "memory");
 }
+__device__ __forceinline__ void mbar_init(uint64_t* m) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(m)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* m, unsigned int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(m)), "r"(bytes) : "memory");
+}
+// Waits until the phase of that parity is over; false where the time limit of every device-side wait ran
+// out (reported; the caller waits no more).
+__device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned int parity, ErrRec* err) {
+  uint64_t t0 = 0;
+  for (unsigned int polls = 1;; ++polls) {
+    unsigned int done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done) : "r"(shared_address(m)), "r"(parity) : "memory");
+    if (done) return true;
+    if ((polls & 63u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > wait_limit_ns(err)) {
+        report(err, LA_ERR_TIMEOUT, SITE_RECURRENCE_ROUND, blockIdx.x, 0);
+        return false;
+      }
+    }
+  }
+}
+// What a CTA keeps of its cluster through the rounds.
+struct Rounds {
+  unsigned int rank, size, n = 0;   // n: rounds so far
+  bool waiting = true;              // until a wait ran out
+};
 
 // Once every warp's (A, H) is in shared memory (H and cut: of the walk's direction): what enters this
 // warp's rows, from what enters the round's tiles, `state`, which becomes what leaves them.
 template <class S, bool CLUSTER, bool BACK, bool MARKED, class M>
-__device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C], const int* cut, int cl, F2& state) {
+__device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C], const int* cut, int cl, F2& state,
+                                         Rounds& rounds, ErrRec* err) {
   const int warp = threadIdx.x >> 5;
   if constexpr (!CLUSTER) {
     F2 h = state;
@@ -367,22 +408,27 @@ __device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C],
       tA = mul2(tA, wA);
       tcut |= r;
     }
-    const unsigned int rank = cluster_rank(), size = cluster_size();
+    const unsigned int rank = rounds.rank, size = rounds.size;
+    uint64_t* arrived = &sm.arrived[buf];
+    if (threadIdx.x == 0) mbar_expect(arrived, size * (S::CL * 16 + 4));
     for (unsigned int to = warp; to < size; to += kWarps) {   // a warp a CTA
       if ((threadIdx.x & 31) < S::CL) {
-        put(&sm.tA[buf][rank][2 * cl], to, tA);
-        put(&sm.tH[buf][rank][2 * cl], to, tH);
-        if (cl == 0) put(&sm.tcut[buf][rank], to, tcut);
+        const unsigned int mbar = at_rank(arrived, to);
+        send(at_rank(&sm.round[buf][rank][cl], to), tA, tH, mbar);
+        if (cl == 0) send(at_rank(&sm.round_cut[buf][rank], to), tcut, mbar);
       }
     }
+    // The buffers take turns: a CTA sends into this one again only after it has had the next round from
+    // everybody, who sent that after reading this one.
+    if (rounds.waiting) rounds.waiting = mbar_wait(arrived, rounds.n >> 1 & 1u, err);
+    ++rounds.n;
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();
     F2 h = state;   // entering the tile
 #pragma unroll 4
     for (unsigned int i = 0; i < size; ++i) {
       if (i == rank) h = state;
-      state = act(sm.tcut[buf][i], load_pair(&sm.tA[buf][i][2 * cl]), load_pair(&sm.tH[buf][i][2 * cl]), state);
+      const ulonglong2 t = sm.round[buf][i][cl];
+      state = act(sm.round_cut[buf][i], F2{t.x}, F2{t.y}, state);
     }
     return act(bcut, bA, bH, h);
   }
@@ -398,7 +444,10 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
   extern __shared__ __align__(16) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<ForwardSmem<S, CLUSTER>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
-  const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;   // tiles a round
+  Rounds rounds;
+  rounds.rank = CLUSTER ? cluster_rank() : 0;
+  rounds.size = CLUSTER ? cluster_size() : 1;
+  const int stride = static_cast<int>(rounds.size);   // tiles a round
   const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
   const bool in = c0 < p.W;
   const int64_t limit = row_limit(p);
@@ -406,16 +455,20 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
   rowless_sequences(p, p.s0, p.s1);
   zero_columns(p, sm, cb * S::C);
   __syncthreads();
-  int t = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  int t = static_cast<int>(rounds.rank);
   auto fetch = [&](int tile, int buf) {
     if (tile < filled) fetch_rows(p, sm, buf, static_cast<int64_t>(tile) * L, cb * S::C, limit);
     commit_rows();   // a group for every call, so that they can be counted
   };
   fetch(t, 0);
   fetch(t + stride, 1);
-  if (CLUSTER) {   // everybody's shared memory is there
-    cluster_arrive();
-    cluster_wait();
+  if (CLUSTER) {   // everybody's mbarriers are there
+    if (tid == 0) {
+      mbar_init(&sm.arrived[0]);
+      mbar_init(&sm.arrived[1]);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cluster_barrier();
   }
   Sequence seq{};
   bool any = true;   // whether the tile has marks
@@ -479,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
       if (lane == 31) sm.cut[buf][warp] = cut;
     }
     __syncthreads();
-    F2 h = fold_warps<S, CLUSTER, false, kMarked>(sm, buf, sm.H[buf], sm.cut[buf], cl, state);
+    F2 h = fold_warps<S, CLUSTER, false, kMarked>(sm, buf, sm.H[buf], sm.cut[buf], cl, state, rounds, p.err);
     if (in && r0 < limit) {
       h = act(ecut, eA, eH, h);
       if (p.ck && row0 % kCkRows == 0 && row0 < limit) {
@@ -510,10 +563,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
     };
     if (now) tile(Yes{}); else tile(No{});
   }
-  if (CLUSTER) {   // nobody leaves while others may still write into its shared memory
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (CLUSTER) cluster_barrier();   // nobody leaves while others may still write into its shared memory
 }
 
 template <class S, bool TIED, bool CLUSTER>
@@ -523,7 +573,10 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<BackwardSmem<S, CLUSTER>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = tid % S::CL, g = tid / S::CL;
-  const int stride = CLUSTER ? static_cast<int>(cluster_size()) : 1;
+  Rounds rounds;
+  rounds.rank = CLUSTER ? cluster_rank() : 0;
+  rounds.size = CLUSTER ? cluster_size() : 1;
+  const int stride = static_cast<int>(rounds.size);
   const int cb = blockIdx.x / stride, c0 = cb * S::C + 2 * cl;
   const bool in = c0 < p.W;
   const int64_t limit = row_limit(p);
@@ -531,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   rowless_sequences(p, p.ds1, p.ds0);
   zero_columns(p, sm, cb * S::C);
   __syncthreads();
-  int k = CLUSTER ? static_cast<int>(cluster_rank()) : 0;   // tiles are counted from the last
+  int k = static_cast<int>(rounds.rank);   // tiles are counted from the last
   auto fetch = [&](int tile, int buf) {
     if (tile < filled) fetch_rows(p, sm, buf, static_cast<int64_t>(filled - 1 - tile) * L, cb * S::C, limit);
     commit_rows();
@@ -539,8 +592,12 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
   fetch(k, 0);
   fetch(k + stride, 1);
   if (CLUSTER) {
-    cluster_arrive();
-    cluster_wait();
+    if (tid == 0) {
+      mbar_init(&sm.arrived[0]);
+      mbar_init(&sm.arrived[1]);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cluster_barrier();
   }
   Sequence seq{};
   bool any = true;
@@ -628,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
       if (lane == 31) sm.cut[buf][warp] = cut;
     }
     __syncthreads();
-    F2 c = fold_warps<S, CLUSTER, true, kMarked>(sm, buf, sm.Cc[buf], sm.ccut[buf], cl, flow);
+    F2 c = fold_warps<S, CLUSTER, true, kMarked>(sm, buf, sm.Cc[buf], sm.ccut[buf], cl, flow, rounds, p.err);
     if (in && rows) {
 #pragma unroll
       for (int w = 0; w < kWarps - 1; ++w)
@@ -676,10 +733,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     };
     if (now) tile(Yes{}); else tile(No{});
   }
-  if (CLUSTER) {
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (CLUSTER) cluster_barrier();
 }
 
 // One token: 14 bytes an element in bf16 (x, f, out, and the fp32 state both ways), nothing else to wait
