@@ -134,7 +134,7 @@ template <class S, int NT, int MOST> struct Smem {
   typename S::T raw[2][NT][S::L][S::C];   // of this tile and the next; each warp's rows are its own
   float A[2][kWarps][S::C], H[2][kWarps][S::C];
   int cut[2][kWarps];                     // whether a sequence starts in the warp's rows
-  int mark[3][S::L];                      // of the tile before, this one and the next: see mark_rows()
+  int mark[S::L];                         // see mark_rows(); each warp's rows are its own
   ulonglong2 round[2][MOST][S::CL];       // (A, H) of the round's tiles, each sent here by its CTA
   int round_cut[2][MOST];
   uint64_t arrived[2];                    // mbarriers: all of a round is here
@@ -212,7 +212,8 @@ __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
   return n < 0 ? 0 : n < p.tokens ? n : p.tokens;
 }
 
-// The sequence a row is in: the first that ends behind the row.
+// The sequence a row is in: the first that ends behind the row, at `from` or later.  A whole warp asks:
+// it looks at 32 sequences at once, and by halves only where the row is far ahead.
 struct Sequence {
   int s;
   int64_t lo, hi;
@@ -225,10 +226,20 @@ __device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, i
     q.hi = q.lo + p.T;
     return q;
   }
+  const int lane = threadIdx.x & 31;
   int a = from, b = p.nseq;
-  while (a < b) {
-    const int mid = (a + b) >> 1;
-    if (__ldg(p.cu + mid + 1) > row) b = mid; else a = mid + 1;
+  while (b - a > 128) {
+    const int mid = (a + b) >> 1, near = a + 64;
+    if (__ldg(p.cu + near) > row) b = near;
+    else if (__ldg(p.cu + mid + 1) > row) b = mid;
+    else a = mid + 1;
+  }
+  for (;; a += 32) {   // ends: behind the last sequence everything is
+    const unsigned int behind = __ballot_sync(0xffffffffu, a + lane >= p.nseq || __ldg(p.cu + a + lane + 1) > row);
+    if (behind) {
+      a += __ffs(behind) - 1;
+      break;
+    }
   }
   q.s = a;
   q.lo = a < p.nseq ? __ldg(p.cu + a) : p.tokens;
@@ -240,23 +251,43 @@ __device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, i
 template <class S> __device__ __forceinline__ bool marked(const Sequence& q, int64_t r0, int64_t limit) {
   return q.lo >= r0 || q.hi <= r0 + S::L || r0 + S::L > limit;
 }
-// Marks a tile's rows: 4 s where sequence s starts or ends, with bit 0 set where it starts and bit 1 where
-// it ends; -1 elsewhere.
+// Marks the warp's rows of a tile: 4 s where sequence s starts or ends, with bit 0 set where it starts and
+// bit 1 where it ends; -1 elsewhere.  `q`: the sequence of the tile's first row.
 constexpr int kStart = 1, kEnd = 2;
 template <class S>
-__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, int from, int* mark) {
-  for (int i = threadIdx.x; i < S::L; i += kThreads) {
-    const int64_t row = r0 + i;
-    int m = -1;
-    if (row < limit) {
-      const Sequence q = sequence_of(p, row, from);
-      if (q.s < p.nseq && q.lo >= 0 && q.lo <= row && q.hi <= p.tokens) {
-        const int at = (q.lo == row ? kStart : 0) | (q.hi - 1 == row ? kEnd : 0);
-        if (at) m = q.s << 2 | at;
-      }
+__device__ __forceinline__ void mark_rows(const RecArgs& p, int64_t r0, int64_t limit, const Sequence& q, int* mark) {
+  constexpr int kWarpRows = S::L / kWarps;
+  const int lane = threadIdx.x & 31, at = (threadIdx.x >> 5) * kWarpRows;
+  const int64_t first = r0 + at;
+  int* own = mark + at;
+  __syncwarp();   // the warp has done with the tile before
+  if (!p.cu) {
+    for (int i = lane; i < kWarpRows; i += 32) {
+      const unsigned int T = p.T, row = static_cast<unsigned int>(first + i), s = row / T, in = row - s * T;
+      const int m = (in == 0 ? kStart : 0) | (in == T - 1 ? kEnd : 0);
+      own[i] = m && first + i < limit ? static_cast<int>(s) << 2 | m : -1;
     }
-    mark[i] = m;
+    __syncwarp();
+    return;
   }
+  for (int i = lane; i < kWarpRows; i += 32) own[i] = -1;
+  __syncwarp();
+  const int64_t end = first + kWarpRows < limit ? first + kWarpRows : limit;
+  for (int s = q.s + lane;; s += 32) {   // a sequence a lane
+    int64_t lo = p.tokens, hi = p.tokens;
+    if (s < p.nseq) {
+      lo = __ldg(p.cu + s);
+      hi = __ldg(p.cu + s + 1);
+    }
+    if (s < p.nseq && lo >= 0 && hi > lo && hi <= p.tokens) {
+      const bool starts = lo >= first && lo < end, ends = hi > first && hi <= end;
+      if (starts) own[lo - first] = s << 2 | kStart | (hi == lo + 1 ? kEnd : 0);
+      if (ends && !(starts && hi == lo + 1)) own[hi - 1 - first] = s << 2 | kEnd;
+    }
+    // until a lane is behind the warp's rows (a malformed order may end this early, or not before the last)
+    if (__any_sync(0xffffffffu, s >= p.nseq || lo >= end)) break;
+  }
+  __syncwarp();
 }
 
 // Sequences without rows: their final state (gradient) is the initial (final) one.  Malformed
@@ -470,33 +501,16 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
     }
     cluster_barrier();
   }
-  Sequence seq{};
-  bool any = true;   // whether the tile has marks
-  if (t < filled) {
-    seq = sequence_of(p, static_cast<int64_t>(t) * L, 0);
-    any = marked<S>(seq, static_cast<int64_t>(t) * L, limit);
-    if (any) mark_rows<S>(p, static_cast<int64_t>(t) * L, limit, p.cu ? seq.s : 0, sm.mark[0]);
-  } else {
-    for (int i = tid; i < L; i += kThreads) sm.mark[0][i] = -1;
-  }
-  __syncthreads();
+  Sequence seq{0, 0, 0};   // of the tile's first row
   F2 state = splat(0.f);   // entering the round's first tile
   // every CTA of a cluster goes through every round, with a tile that has rows or without
-  for (int buf = 0, slot = 0; t - t % stride < filled; t += stride, buf ^= 1) {
+  for (int buf = 0; t - t % stride < filled; t += stride, buf ^= 1) {
     const int64_t r0 = static_cast<int64_t>(t) * L, row0 = r0 + g * R;
-    const int* mark = sm.mark[slot] + g * R;
-    slot = slot == 2 ? 0 : slot + 1;
-    const bool now = any;
-    // the next tile's marks, before the barrier; nobody reads those of the tile before the last any more
-    if (t + stride < filled) {
-      const int64_t next = r0 + static_cast<int64_t>(stride) * L;
-      if (seq.hi <= next) seq = sequence_of(p, next, p.cu ? seq.s : 0);
-      any = marked<S>(seq, next, limit);
-      if (any) mark_rows<S>(p, next, limit, p.cu ? seq.s : 0, sm.mark[slot]);
-    } else {
-      any = true;   // a round without a tile
-      for (int i = tid; i < L; i += kThreads) sm.mark[slot][i] = -1;
-    }
+    const int* mark = sm.mark + g * R;
+    const bool rows = t < filled;   // a CTA without a tile in the last round takes part with an empty one
+    if (rows && seq.hi <= r0) seq = sequence_of(p, r0, p.cu ? seq.s : 0);
+    const bool now = !rows || marked<S>(seq, r0, limit);
+    if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {   // the marks' tests are kept out of the common case
     constexpr bool kMarked = decltype(with_marks)::value;
     const T* x = &sm.raw[buf][0][g * R][2 * cl];
@@ -599,33 +613,15 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     }
     cluster_barrier();
   }
-  Sequence seq{};
-  bool any = true;
-  if (k < filled) {
-    const int64_t r0 = static_cast<int64_t>(filled - 1 - k) * L;
-    seq = sequence_of(p, r0, 0);
-    any = marked<S>(seq, r0, limit);
-    if (any) mark_rows<S>(p, r0, limit, p.cu ? seq.s : 0, sm.mark[0]);
-  } else {
-    for (int i = tid; i < L; i += kThreads) sm.mark[0][i] = -1;
-  }
-  __syncthreads();
+  Sequence seq{0, p.tokens, 0};   // of the tile's first row
   F2 flow = splat(0.f);   // entering the round's first tile from behind
-  for (int buf = 0, slot = 0; k - k % stride < filled; k += stride, buf ^= 1) {
+  for (int buf = 0; k - k % stride < filled; k += stride, buf ^= 1) {
     const bool rows = k < filled;   // a CTA without a tile in the last round takes part with an empty one
     const int64_t r0 = rows ? static_cast<int64_t>(filled - 1 - k) * L : limit, row0 = r0 + g * R;
-    const int* mark = sm.mark[slot] + g * R;
-    slot = slot == 2 ? 0 : slot + 1;
-    const bool now = any;
-    if (k + stride < filled) {   // the next tile's marks
-      const int64_t next = r0 - static_cast<int64_t>(stride) * L;
-      if (seq.lo > next) seq = sequence_of(p, next, 0);
-      any = marked<S>(seq, next, limit);
-      if (any) mark_rows<S>(p, next, limit, p.cu ? seq.s : 0, sm.mark[slot]);
-    } else {
-      any = true;
-      for (int i = tid; i < L; i += kThreads) sm.mark[slot][i] = -1;
-    }
+    const int* mark = sm.mark + g * R;
+    if (rows && seq.lo > r0) seq = sequence_of(p, r0, 0);
+    const bool now = !rows || marked<S>(seq, r0, limit);
+    if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {
     constexpr bool kMarked = decltype(with_marks)::value;
     const T* x = &sm.raw[buf][0][g * R][2 * cl];
