@@ -422,9 +422,9 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
  *   a_t = sigmoid(f_t),   b_t = x_t (PLAIN) or (1 - a_t) x_t (TIED),
  *   h_t = a_t h_{t-1} + b_t,   h_0 = state_in (zeros if NULL),   out_t = h_t.
  * Gates, products of gates and states are held in fp32; out is rounded once, from the fp32
- * state.  The time axis is cut into blocks of rows that are worked on at the same time, so
- * the result depends on where a sequence starts in the packed rows by fp32 rounding only; it
- * is the same for every call with the same arguments.
+ * state.  The rows are worked on in tiles, many at the same time, so the result depends on
+ * where a sequence starts in the packed rows, and on the other arguments' sizes, by fp32
+ * rounding only; it is the same for every call with the same arguments.
  *
  *   x, f, out    [B, T, W] dtype (x and f read only; out may not alias them).
  *   state_in     fp32 [B, W] initial state per sequence, or NULL for zeros.
@@ -437,9 +437,11 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
  *                element by element (slower, same results).
  *   workspace    device scratch of >= lightning_attn_gated_recurrence_workspace_size bytes,
  *                256-byte aligned, its first 256 bytes (the error record, as for the
- *                prefill) zero before its first use.
- * f = +inf keeps the state (a = 1), f = -inf drops it (a = 0).  A NaN, or a state that left
- * the fp32 range, stays in its own channel of its own sequence (an infinity may become NaN).
+ *                prefill) zero before its first use; the call uses the rest only where
+ *                state_out overlaps state_in (a copy).
+ * f = +inf keeps the state (a = 1); f below -87.3 drops it (a = 0).  A NaN, or a state that
+ * left the fp32 range, stays in its own channel of its own sequence (an infinity may become
+ * NaN).
  * Returns LA_OK after enqueueing, or an error status with nothing enqueued.
  */
 typedef enum { LA_INPUT_PLAIN = 0, LA_INPUT_TIED = 1 } la_input_mode;
@@ -454,8 +456,10 @@ LA_API la_status lightning_attn_gated_recurrence(const void* x, const void* f, v
 /*
  * The gated recurrence over N packed sequences (cu_seqlens DEVICE int32 [N + 1] as for
  * lightning_attn_prefill_varlen; x, f, out [total_tokens, W]; states fp32 [N, W]).  Empty
- * sequences are allowed (state_out = state_in or zeros); rows behind cu_seqlens[N] are left
- * as they were.  Violations found on the device are reported by lightning_attn_check.
+ * sequences are allowed (state_out = state_in or zeros).  cu_seqlens[N] may be below
+ * total_tokens: rows behind it are left as they were (in the backward too).  Violations found
+ * on the device are reported by lightning_attn_check; what the rows of a malformed batch
+ * receive is then unspecified.
  */
 LA_API la_status lightning_attn_gated_recurrence_varlen(const void* x, const void* f, void* out,
                                                         const float* state_in, float* state_out,
@@ -506,7 +510,8 @@ LA_API la_status lightning_attn_gated_recurrence_backward_varlen(
 /*
  * Workspace bytes of the gated recurrence's calls over num_seqs sequences (B, or N) of
  * total_tokens packed rows (B * T) of W channels; backward: 0 for the forward calls, 1 for
- * the backward ones (which also serves the forward).  0 on invalid arguments.
+ * the backward ones (which also serves the forward and includes room for the checkpoints).
+ * 0 on invalid arguments.
  */
 LA_API size_t lightning_attn_gated_recurrence_workspace_size(int num_seqs, int total_tokens, int W, la_dtype dtype,
                                                              int backward);

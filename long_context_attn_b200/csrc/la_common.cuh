@@ -33,7 +33,6 @@ enum Site : unsigned int {
   SITE_TC_NORM_WAIT = 6,
   SITE_VARLEN_CU = 7,
   SITE_TC_TEARDOWN = 8,
-  SITE_RECURRENCE_ROUND = 9,
 };
 
 enum Inject : unsigned int {

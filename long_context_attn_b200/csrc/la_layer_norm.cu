@@ -407,21 +407,6 @@ __global__ void __launch_bounds__(1024) layer_norm_weight_sum_kernel(const float
   }
 }
 
-#ifndef FT
-#define FT 512
-#endif
-#ifndef BT
-#define BT 512
-#endif
-#ifndef BT8
-#define BT8 1024
-#endif
-#ifndef BT12
-#define BT12 640
-#endif
-#ifndef FSTAY
-#define FSTAY 256
-#endif
 constexpr int kMaxParts = 1184;   // CTAs of the backward pass: at most 8 for each of 148 SMs
 
 struct LnArgs {
@@ -454,8 +439,8 @@ template <class R, bool RES> cudaError_t ln_forward(const LnArgs& a) {
   constexpr int G = R::G, TPB = G == 32 ? 128 : G;
   // wide rows: CTAs that stay, 512 threads an SM, their shared memory full of rows to come;
   // narrow ones: a row a group, as many as fit
-  constexpr bool kStay = R::V > 1 && G >= FSTAY;
-  constexpr int BLOCKS = kStay ? (FT / TPB > 0 ? FT / TPB : 1) : 1;
+  constexpr bool kStay = R::V > 1 && G >= 256;
+  constexpr int BLOCKS = kStay ? (512 / TPB > 0 ? 512 / TPB : 1) : 1;
   constexpr int SLOTS = kStay ? clamp_slots(200 * 1024 / (BLOCKS * TPB) / 16 / ((RES ? 2 : 1) * R::NV)) : 0;
   constexpr size_t smem = Ring<R, TPB, RES ? 2 : 1, SLOTS>::kBytes;
   auto kernel = layer_norm_kernel<R, TPB, RES, SLOTS, BLOCKS>;
@@ -472,7 +457,8 @@ template <class R, bool RES> cudaError_t ln_forward(const LnArgs& a) {
 template <class R, bool SUM> cudaError_t ln_backward(const LnArgs& a) {
   using T = typename R::T;
   constexpr int G = R::G, TPB = G == 32 ? 256 : G, per = TPB / G;
-  constexpr int THREADS = R::NV * R::V <= 8 ? BT8 : R::NV * R::V <= 12 ? BT12 : BT;   // an SM, by the registers of the sums
+  constexpr int kValues = R::NV * R::V;   // of a row, and of each sum, in a thread
+  constexpr int THREADS = kValues <= 8 ? 1024 : kValues <= 12 ? 640 : 512;   // an SM, by the registers of the sums
   constexpr int BLOCKS = THREADS / TPB > 0 ? THREADS / TPB : 1;
   constexpr int SLOTS = R::V == 1 ? 0 : clamp_slots(200 * 1024 / (BLOCKS * TPB) / 16 / ((SUM ? 3 : 2) * R::NV));
   constexpr size_t ring = Ring<R, TPB, SUM ? 3 : 2, SLOTS>::kBytes;

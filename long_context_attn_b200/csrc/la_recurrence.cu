@@ -31,6 +31,10 @@ namespace {
 
 constexpr int kCkRows = LA_RECURRENCE_CHECKPOINT_ROWS;
 constexpr int kMaxCluster = 16, kMaxBackCluster = 8;   // the backward's fill the shared memory of two CTAs an SM
+// The error record's site of a round that did not arrive (the tensor-core kernels' are 1 to 8), and the
+// fault that makes the first CTA of a walk in clusters send nothing, so that its cluster's waits must run
+// out (theirs is 1).
+constexpr unsigned int kSiteRound = 9, kInjectSilent = 2;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 struct RecArgs {
@@ -399,7 +403,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned int parity, ErrR
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
       if (now - t0 > wait_limit_ns(err)) {
-        report(err, LA_ERR_TIMEOUT, SITE_RECURRENCE_ROUND, blockIdx.x, 0);
+        report(err, LA_ERR_TIMEOUT, kSiteRound, blockIdx.x, 0);
         return false;
       }
     }
@@ -409,6 +413,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned int parity, ErrR
 struct Rounds {
   unsigned int rank, size, n = 0;   // n: rounds so far
   bool waiting = true;              // until a wait ran out
+  bool silent = false;              // a failure test's: sends nothing
 };
 
 // Once every warp's (A, H) is in shared memory (H and cut: of the walk's direction): what enters this
@@ -441,8 +446,8 @@ __device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C],
     }
     const unsigned int rank = rounds.rank, size = rounds.size;
     uint64_t* arrived = &sm.arrived[buf];
-    if (threadIdx.x == 0) mbar_expect(arrived, size * (S::CL * 16 + 4));
-    for (unsigned int to = warp; to < size; to += kWarps) {   // a warp a CTA
+    if (threadIdx.x == 0 && rounds.waiting) mbar_expect(arrived, size * (S::CL * 16 + 4));   // once a phase
+    for (unsigned int to = rounds.silent ? size : warp; to < size; to += kWarps) {   // a warp a CTA
       if ((threadIdx.x & 31) < S::CL) {
         const unsigned int mbar = at_rank(arrived, to);
         send(at_rank(&sm.round[buf][rank][cl], to), tA, tH, mbar);
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
       mbar_init(&sm.arrived[1]);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    rounds.silent = blockIdx.x == 0 && p.err->inject == kInjectSilent;
     cluster_barrier();
   }
   Sequence seq{0, 0, 0};   // of the tile's first row
@@ -611,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
       mbar_init(&sm.arrived[1]);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    rounds.silent = blockIdx.x == 0 && p.err->inject == kInjectSilent;
     cluster_barrier();
   }
   Sequence seq{0, p.tokens, 0};   // of the tile's first row

@@ -4,16 +4,21 @@ bounds on the error that fp32 arithmetic and one rounding to the output type can
 Every bound is a first-order sum over the roundings of the computation, u = 2^-24 being the
 relative error of one fp32 operation:
 
-  gate   e = exp(-|f|) is off by at most 2 ulp (4u, the bound CUDA states for expf); 1 + e,
-         the reciprocal and the product add one u each, so a and 1 - a are within 8u.
-  scan   h_t is a sum of terms (a_{s+1} .. a_t) b_s.  A term takes at most t - s + 1 gates and
-         products, each within 8u + u whatever their order (a tree over blocks multiplies the
-         same factors), and its b (within 9u): (t - s + 1) * 16u covers them.  With
-         M_t = a_t M_{t-1} + |b_t| and N_t = a_t N_{t-1} + M_t (so that N_t = sum over s of
-         (t - s + 1) times the term's size) that is 16u N_t.  Adding the terms up, in any
-         order, rounds each partial sum once per level; the at most 128 + 40 levels of a block
-         and of the tree above it are inside 200u M_t, and chains over more blocks round in
-         proportion to (t - s + 1), inside 16u N_t.
+  gate   t = exp(-f) is off by at most 4u with expf (2 ulp, the bound CUDA states), and by (4 + |f|)u
+         where exp2 is taken of the rounded product -f log2(e) (bf16 gates). 1 + t adds u, the
+         reciprocal after its Newton step 2u, a product u. t's error reaches a = 1 / (1 + t) times
+         t / (1 + t): for f >= 0 that is at most 2u + 0.28u (|f| t / (1 + t) <= 0.28), so a is
+         within 6u there, and a for f < 0 and 1 - a within (8 + |f|)u.
+  scan   h_t is a sum of terms (a_{s+1} .. a_t) b_s.  A term takes at most t - s + 1 gates and as many
+         products, whatever their order (a tree over tiles multiplies the same factors): 16u for
+         each covers 6u + u, and gates down to f = -9. What gates below that add, |f| - 9 each, sums
+         to less than 88u as long as the term is a normal fp32 number (its size is at most the product
+         of their exp(-|f|) > 2^-126 = exp(-87.3)). With M_t = a_t M_{t-1} + |b_t| and
+         N_t = a_t N_{t-1} + M_t (so that N_t = sum over s of (t - s + 1) times the term's size) all of
+         it is inside 16u N_t + 88u M_t. Adding the terms up rounds each partial sum once per level:
+         at most 16 rows of a thread, 3 of a warp's groups, 8 warps and 16 tiles of a round, 43 levels;
+         88u + 43u < 200u M_t.  Further tiles add a level for each 128 rows or more, inside the spare
+         of 16u for each row.
   out    one rounding to the output type: half an eps of the value.
 """
 from __future__ import annotations
@@ -97,9 +102,9 @@ def packed(x, f, lens, tied, s0=None, dout=None, ds1=None):
 
 def layer_norm(s, w, b, eps, dout=None, dsum=None):
     """Rows s [rows, W] (fp64): dict of out and, with dout, dx, dweight, dbias, each with its
-    bound.  A sum of W values takes at most 16 (a thread's) + 5 + 32 roundings of partial sums
-    over 16 values a thread (64 for widths above 8192): 128u of the sum of sizes covers it.
-    sqrt and the divisions are IEEE-rounded: r is within 8u more than half the variance's."""
+    bound.  A sum of W values rounds partial sums at most 32 times in a thread (16 vectors of one
+    value, or 4 of 8 in pairs), 5 in a warp and 5 over the warps: 128u of the sum of sizes covers
+    it. sqrt and the divisions are IEEE-rounded: r is within 8u more than half the variance's."""
     rows, W = s.shape
     k = 128 * U
     mean = s.mean(1, keepdims=True)

@@ -378,6 +378,34 @@ def test_malformed_offsets_are_reported(cuda_device):
     la.lightning_attn_check(ws)        # the workspace is usable again
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_missing_sum_runs_into_the_time_limit(backward, cuda_device):
+    """A CTA that sends nothing: the waits of its cluster run out after the limit that the workspace
+    sets, the error is reported, the GPU stays usable and so does the workspace."""
+    torch, la = _torch()
+    T, W = 4096, 64
+    x = torch.randn(1, T, W, device="cuda").bfloat16()
+    out, dx, df = (torch.empty_like(x) for _ in range(3))
+    ws = _ws(la, 1, T, W, x, True)
+    ck = la.new_recurrence_checkpoints(T, W).zero_()
+
+    def call():
+        if backward:
+            la.lightning_attn_gated_recurrence_backward(x, x, x, dx, df, checkpoints=ck, workspace=ws)
+        else:
+            la.lightning_attn_gated_recurrence(x, x, out, workspace=ws)
+
+    words = ws[:256].view(torch.int32)
+    words[4], words[5] = 50, 2          # milliseconds, the fault
+    call()
+    with pytest.raises(la.LightningAttnError) as err:
+        la.lightning_attn_check(ws)
+    assert err.value.status == la.LA_ERR_TIMEOUT
+    words[4:6] = 0
+    call()
+    la.lightning_attn_check(ws)
+
+
 def test_streams_and_graphs(cuda_device):
     """Two calls at once on two streams with a workspace each, and both captured into graphs that
     share one workspace and are replayed in turn on new inputs."""
