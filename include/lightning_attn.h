@@ -432,9 +432,10 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
  *   checkpoints  fp32 [ceil(B*T / LA_RECURRENCE_CHECKPOINT_ROWS), W], or NULL: written with
  *                the fp32 state that each LA_RECURRENCE_CHECKPOINT_ROWS-th packed row starts
  *                from, for lightning_attn_gated_recurrence_backward.
- *   B, T, W      B >= 1, T >= 0 (T == 0: no output; state_out = state_in or zeros), W >= 1.
- *                Rows whose bytes are a multiple of 16 are read as 16-byte vectors; others
- *                element by element (slower, same results).
+ *   B, T, W      B >= 1, T >= 0 (T == 0: no output; state_out = state_in or zeros), W >= 1
+ *                (LA_ERR_UNSUPPORTED: B > 2^28, W > 2^22, B*T > 2^31 - 1).  Rows whose bytes
+ *                are a multiple of 16 are read as 16-byte vectors; others element by element
+ *                (slower, same results).
  *   workspace    device scratch of >= lightning_attn_gated_recurrence_workspace_size bytes,
  *                256-byte aligned, its first 256 bytes (the error record, as for the
  *                prefill) zero before its first use; the call uses the rest only where

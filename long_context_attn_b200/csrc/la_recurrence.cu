@@ -216,13 +216,13 @@ __device__ __forceinline__ int64_t row_limit(const RecArgs& p) {
   return n < 0 ? 0 : n < p.tokens ? n : p.tokens;
 }
 
-// The sequence a row is in: the first that ends behind the row, at `from` or later.  A whole warp asks:
+// The sequence a row is in: the first that ends behind the row, from `from` to `to`.  A whole warp asks:
 // it looks at 32 sequences at once, and by halves only where the row is far ahead.
 struct Sequence {
   int s;
   int64_t lo, hi;
 };
-__device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, int from) {
+__device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, int from, int to) {
   Sequence q;
   if (!p.cu) {
     q.s = static_cast<int>(static_cast<unsigned int>(row) / static_cast<unsigned int>(p.T));   // row < tokens <= INT32_MAX
@@ -231,7 +231,7 @@ __device__ __forceinline__ Sequence sequence_of(const RecArgs& p, int64_t row, i
     return q;
   }
   const int lane = threadIdx.x & 31;
-  int a = from, b = p.nseq;
+  int a = from, b = to;
   while (b - a > 128) {
     const int mid = (a + b) >> 1, near = a + 64;
     if (__ldg(p.cu + near) > row) b = near;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
     const int64_t r0 = static_cast<int64_t>(t) * L, row0 = r0 + g * R;
     const int* mark = sm.mark + g * R;
     const bool rows = t < filled;   // a CTA without a tile in the last round takes part with an empty one
-    if (rows && seq.hi <= r0) seq = sequence_of(p, r0, p.cu ? seq.s : 0);
+    if (rows && seq.hi <= r0) seq = sequence_of(p, r0, seq.s, p.nseq);
     const bool now = !rows || marked<S>(seq, r0, limit);
     if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {   // the marks' tests are kept out of the common case
@@ -620,13 +620,20 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     rounds.silent = blockIdx.x == 0 && p.err->inject == kInjectSilent;
     cluster_barrier();
   }
-  Sequence seq{0, p.tokens, 0};   // of the tile's first row
+  Sequence seq{p.nseq, p.tokens, 0};   // of the tile's first row
   F2 flow = splat(0.f);   // entering the round's first tile from behind
   for (int buf = 0; k - k % stride < filled; k += stride, buf ^= 1) {
     const bool rows = k < filled;   // a CTA without a tile in the last round takes part with an empty one
     const int64_t r0 = rows ? static_cast<int64_t>(filled - 1 - k) * L : limit, row0 = r0 + g * R;
     const int* mark = sm.mark + g * R;
-    if (rows && seq.lo > r0) seq = sequence_of(p, r0, 0);
+    if (rows && seq.lo > r0) {
+      int from = 0, to = seq.s;
+      if (p.cu) {   // near the one before, mostly
+        const int near = to > 62 ? to - 62 : 0;
+        if (__ldg(p.cu + near) <= r0) from = near; else to = near;
+      }
+      seq = sequence_of(p, r0, from, to);
+    }
     const bool now = !rows || marked<S>(seq, r0, limit);
     if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {
@@ -920,7 +927,8 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
                      cudaStream_t stream) {
   if ((dt != LA_F32 && dt != LA_BF16) || (mode != LA_INPUT_PLAIN && mode != LA_INPUT_TIED)) return LA_ERR_INVALID_ARG;
   if (p.nseq < 1 || p.W < 1 || p.tokens < 0) return LA_ERR_INVALID_ARG;
-  if (p.tokens > INT32_MAX || p.nseq > (1 << 28)) return LA_ERR_UNSUPPORTED;   // marks hold a sequence and two bits
+  // marks hold a sequence and two bits; offsets inside a tile are 32-bit
+  if (p.tokens > INT32_MAX || p.nseq > (1 << 28) || p.W > (1 << 22)) return LA_ERR_UNSUPPORTED;
   if (p.tokens > 0) {
     const void* in[3] = {p.x, p.f, p.dout};
     void* out[2] = {backward ? p.dx : p.out, p.df};

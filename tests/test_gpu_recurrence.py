@@ -53,6 +53,9 @@ LENS = {
     "blocks": [256, 512, 128, 1, 255, 384],
     "many": [int(n) for n in np.random.default_rng(1).integers(0, 9, 200)],
     "long": [3, 2900, 0, 41],
+    "thousands": [int(n) for n in np.random.default_rng(2).integers(0, 4, 4000)],
+    "sparse": [0] * 700 + [600] + [0] * 900 + [1] + [0] * 40 + [300, 2, 0],
+    "none": [0, 0, 0],
 }
 
 FIXED = [(1, 1, 64), (1, 2, 8), (3, 1, 128), (1, 127, 64), (1, 128, 64), (1, 129, 64), (2, 257, 72), (5, 100, 200),

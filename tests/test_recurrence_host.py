@@ -114,6 +114,9 @@ def test_recurrence_entries_refuse(lib):
             assert call(fn, packed, backward, **kw) == 1, (packed, backward, kw)
     assert call(fwd, 0, 0, n=1 << 20, T=1 << 12) == 2       # 2^32 rows
     assert call(bwd, 0, 1, n=1 << 20, T=1 << 12) == 2
+    for fn, packed, backward in ((fwd, 0, 0), (var, 1, 0), (bwd, 0, 1), (bvar, 1, 1)):
+        assert call(fn, packed, backward, W=(1 << 22) + 1) == 2
+        assert call(fn, packed, backward, n=(1 << 28) + 1, T=1) == 2
 
     for kw in (dict(x=None), dict(f=ODD), dict(out=p[0]), dict(out=p[1]), dict(st=None), dict(st=ODD), dict(B=0),
                dict(W=0), dict(dt=5), dict(mode=3)):
