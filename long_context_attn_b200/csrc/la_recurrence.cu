@@ -62,9 +62,9 @@ struct RecArgs {
 // and an IEEE division the first tiled kernel spent 47 instructions an element and ran at 0.30
 // of the HBM rate, instruction-bound); fp32 gates call expf.  A Newton-Raphson step
 // brings the approximate reciprocal to a correctly rounded one in nearly all cases: with the approximate
-// one alone, states that remember 1000 tokens were 3 times as far off as with an IEEE division.  t is held to 2^126 (f < -87.3), so
-// that 1 / (1 + t) stays a normal number and keep = 1 there; taking 2^-126 away from it makes a 0
-// there and changes no a above 2^-101.  A NaN passes.
+// one alone, states that remember 1000 tokens were 3 times as far off as with an IEEE division.  t is
+// held to 2^126 (f < -87.3), so that 1 / (1 + t) stays a normal number and keep = 1 there; taking
+// 2^-126 away from it makes a 0 there and changes no a above 2^-101.  A NaN passes.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -524,13 +524,13 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
     const bool now = !rows || marked<S>(seq, r0, limit);
     if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {   // the marks' tests are kept out of the common case
-    constexpr bool kMarked = decltype(with_marks)::value;
-    const T* x = &sm.raw[buf][0][g * R][2 * cl];
-    const T* f = &sm.raw[buf][1][g * R][2 * cl];
-    rows_here();
+      constexpr bool kMarked = decltype(with_marks)::value;
+      const T* x = &sm.raw[buf][0][g * R][2 * cl];
+      const T* f = &sm.raw[buf][1][g * R][2 * cl];
+      rows_here();
 
-    F2 a[R], b[R], A = splat(1.f), H = splat(0.f);
-    int cut = 0;
+      F2 a[R], b[R], A = splat(1.f), H = splat(0.f);
+      int cut = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if constexpr (kMarked) {
@@ -547,29 +547,29 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
         H = fma2(a[i], H, b[i]);
         A = mul2(A, a[i]);
       }
-    __syncwarp();   // the warp's rows have been read
-    fetch(t + 2 * stride, buf);
-    F2 eA, eH;
-    int ecut;
-    compose_warp<S::CL, false>(A, H, cut, eA, eH, ecut);
-    if (lane >= 32 - S::CL) {
-      *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
-      *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
-      if (lane == 31) sm.cut[buf][warp] = cut;
-    }
-    __syncthreads();
-    F2 h = fold_warps<S, CLUSTER, false, kMarked>(sm, buf, sm.H[buf], sm.cut[buf], cl, state, rounds, p.err);
-    if (in && r0 < limit) {
-      h = act(ecut, eA, eH, h);
-      if (p.ck && row0 % kCkRows == 0 && row0 < limit) {
-        const int m = kMarked ? mark[0] : -1;
-        const bool first = m >= 0 && (m & kStart);
-        store_pair<S::VEC>(p.ck + row0 / kCkRows * p.W + c0, first ? state_or_zero<S::VEC>(p.s0, m >> 2, c0, p.W) : h, c0, p.W);
+      __syncwarp();   // the warp's rows have been read
+      fetch(t + 2 * stride, buf);
+      F2 eA, eH;
+      int ecut;
+      compose_warp<S::CL, false>(A, H, cut, eA, eH, ecut);
+      if (lane >= 32 - S::CL) {
+        *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
+        *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
+        if (lane == 31) sm.cut[buf][warp] = cut;
       }
-      if (p.out) {   // else the checkpoints are all that is wanted
-        // a base the whole CTA shares and 32-bit offsets from it (L * W < 2^31)
-        T* out = static_cast<T*>(p.out) + r0 * p.W + cb * S::C;
-        unsigned int at = static_cast<unsigned int>(g * R) * static_cast<unsigned int>(p.W) + 2 * cl;
+      __syncthreads();
+      F2 h = fold_warps<S, CLUSTER, false, kMarked>(sm, buf, sm.H[buf], sm.cut[buf], cl, state, rounds, p.err);
+      if (in && r0 < limit) {
+        h = act(ecut, eA, eH, h);
+        if (p.ck && row0 % kCkRows == 0 && row0 < limit) {
+          const int m = kMarked ? mark[0] : -1;
+          const bool first = m >= 0 && (m & kStart);
+          store_pair<S::VEC>(p.ck + row0 / kCkRows * p.W + c0, first ? state_or_zero<S::VEC>(p.s0, m >> 2, c0, p.W) : h, c0, p.W);
+        }
+        if (p.out) {   // else the checkpoints are all that is wanted
+          // a base the whole CTA shares and 32-bit offsets from it (L * W < 2^31)
+          T* out = static_cast<T*>(p.out) + r0 * p.W + cb * S::C;
+          unsigned int at = static_cast<unsigned int>(g * R) * static_cast<unsigned int>(p.W) + 2 * cl;
 #pragma unroll
           for (int i = 0; i < R; ++i, at += p.W) {
             if constexpr (kMarked) {
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
               if (m >= 0 && (m & kEnd) && p.s1) store_pair<S::VEC>(p.s1 + static_cast<int64_t>(m >> 2) * p.W + c0, h, c0, p.W);
             }
           }
+        }
       }
-    }
     };
     if (now) tile(Yes{}); else tile(No{});
   }
@@ -643,20 +643,20 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     const bool now = !rows || marked<S>(seq, r0, limit);
     if (now) mark_rows<S>(p, r0, limit, seq, sm.mark);
     auto tile = [&](auto with_marks) {
-    constexpr bool kMarked = decltype(with_marks)::value;
-    const T* x = &sm.raw[buf][0][g * R][2 * cl];
-    const T* f = &sm.raw[buf][1][g * R][2 * cl];
-    const T* d = &sm.raw[buf][2][g * R][2 * cl];
-    F2 hin = splat(0.f);   // the state entering the tile
-    if (in && rows) hin = load_state<S::VEC>(p.ck + r0 / kCkRows * p.W + c0, c0, p.W);
-    rows_here();
+      constexpr bool kMarked = decltype(with_marks)::value;
+      const T* x = &sm.raw[buf][0][g * R][2 * cl];
+      const T* f = &sm.raw[buf][1][g * R][2 * cl];
+      const T* d = &sm.raw[buf][2][g * R][2 * cl];
+      F2 hin = splat(0.f);   // the state entering the tile
+      if (in && rows) hin = load_state<S::VEC>(p.ck + r0 / kCkRows * p.W + c0, c0, p.W);
+      rows_here();
 
-    // What the group's rows do to the state, and to the flow into the state before them: C grows with
-    // each row by the row's own part, carried over the rows before it (and the row) by A.  Every Q rows,
-    // what the rows so far do to the state is kept.
-    F2 a[R], keep[R], A = splat(1.f), H = splat(0.f), C = splat(0.f), qA[NQ], qH[NQ];
-    int cut = 0, ccut = 0;
-    unsigned int qcut = 0;
+      // What the group's rows do to the state, and to the flow into the state before them: C grows with
+      // each row by the row's own part, carried over the rows before it (and the row) by A.  Every Q rows,
+      // what the rows so far do to the state is kept.
+      F2 a[R], keep[R], A = splat(1.f), H = splat(0.f), C = splat(0.f), qA[NQ], qH[NQ];
+      int cut = 0, ccut = 0;
+      unsigned int qcut = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (i % Q == 0) {
@@ -685,32 +685,32 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
         const F2 xv = load_pair(x + i * S::C);
         H = fma2(a[i], H, TIED ? mul2(keep[i], xv) : xv);
       }
-    const F2 gA = A;   // the group's own
-    F2 eA = splat(1.f), eH = splat(0.f), bA, bC;
-    int ecut = 0, bcut;
-    F2 wA = gA;
-    compose_warp<S::CL, false>(wA, H, cut, eA, eH, ecut);
-    compose_warp<S::CL, true>(A, C, ccut, bA, bC, bcut);
-    if (lane < S::CL) {   // all groups, from the last
-      *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
-      *reinterpret_cast<F2*>(&sm.Cc[buf][warp][2 * cl]) = C;
-      if (lane == 0) sm.ccut[buf][warp] = ccut;
-    }
-    if (lane >= 32 - S::CL) {
-      *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
-      if (lane == 31) sm.cut[buf][warp] = cut;
-    }
-    __syncthreads();
-    F2 c = fold_warps<S, CLUSTER, true, kMarked>(sm, buf, sm.Cc[buf], sm.ccut[buf], cl, flow, rounds, p.err);
-    if (in && rows) {
+      const F2 gA = A;   // the group's own
+      F2 eA = splat(1.f), eH = splat(0.f), bA, bC;
+      int ecut = 0, bcut;
+      F2 wA = gA;
+      compose_warp<S::CL, false>(wA, H, cut, eA, eH, ecut);
+      compose_warp<S::CL, true>(A, C, ccut, bA, bC, bcut);
+      if (lane < S::CL) {   // all groups, from the last
+        *reinterpret_cast<F2*>(&sm.A[buf][warp][2 * cl]) = A;
+        *reinterpret_cast<F2*>(&sm.Cc[buf][warp][2 * cl]) = C;
+        if (lane == 0) sm.ccut[buf][warp] = ccut;
+      }
+      if (lane >= 32 - S::CL) {
+        *reinterpret_cast<F2*>(&sm.H[buf][warp][2 * cl]) = H;
+        if (lane == 31) sm.cut[buf][warp] = cut;
+      }
+      __syncthreads();
+      F2 c = fold_warps<S, CLUSTER, true, kMarked>(sm, buf, sm.Cc[buf], sm.ccut[buf], cl, flow, rounds, p.err);
+      if (in && rows) {
 #pragma unroll
-      for (int w = 0; w < kWarps - 1; ++w)
-        if (w < warp) hin = act(kMarked ? sm.cut[buf][w] : 0, load_pair(&sm.A[buf][w][2 * cl]), load_pair(&sm.H[buf][w][2 * cl]), hin);
-      hin = act(ecut, eA, eH, hin);
-      c = act(bcut, bA, bC, c);
-      T* dx = static_cast<T*>(p.dx) + r0 * p.W + cb * S::C;
-      T* df = static_cast<T*>(p.df) + r0 * p.W + cb * S::C;
-      unsigned int at = static_cast<unsigned int>(g * R + R - 1) * static_cast<unsigned int>(p.W) + 2 * cl;
+        for (int w = 0; w < kWarps - 1; ++w)
+          if (w < warp) hin = act(kMarked ? sm.cut[buf][w] : 0, load_pair(&sm.A[buf][w][2 * cl]), load_pair(&sm.H[buf][w][2 * cl]), hin);
+        hin = act(ecut, eA, eH, hin);
+        c = act(bcut, bA, bC, c);
+        T* dx = static_cast<T*>(p.dx) + r0 * p.W + cb * S::C;
+        T* df = static_cast<T*>(p.df) + r0 * p.W + cb * S::C;
+        unsigned int at = static_cast<unsigned int>(g * R + R - 1) * static_cast<unsigned int>(p.W) + 2 * cl;
 #pragma unroll
         for (int q = NQ - 1; q >= 0; --q) {
           F2 h = act(qcut >> q & 1u, qA[q], qH[q], hin), prev[Q];
@@ -743,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
             }
           }
         }
-    }
-    __syncwarp();   // the warp's rows have been read to the end
-    fetch(k + 2 * stride, buf);
+      }
+      __syncwarp();   // the warp's rows have been read to the end
+      fetch(k + 2 * stride, buf);
     };
     if (now) tile(Yes{}); else tile(No{});
   }
