@@ -419,8 +419,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned int parity, ErrR
 struct Rounds {
   unsigned int rank, size, n = 0;   // n: rounds so far
   bool waiting = true;              // until a wait ran out
-  bool silent = false;              // a failure test's: sends nothing
+  bool silent = false;              // sends nothing: its wait ran out (or a failure test says so)
 };
+// The end of a cluster's walk: nobody leaves while others may still send into its shared memory.  Who had
+// every round has had all that was sent to it.  Where a wait ran out, sends may be on their way that nothing
+// counts any more; all of them were issued before the barrier, so the CTA stays for another millisecond, a
+// thousand times what they take.
+__device__ __forceinline__ void leave_cluster(const Rounds& rounds) {
+  cluster_barrier();
+  if (rounds.waiting) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
 
 // Once every warp's (A, H) is in shared memory (H and cut: of the walk's direction): what enters this
 // warp's rows, from what enters the round's tiles, `state`, which becomes what leaves them.
@@ -462,7 +472,10 @@ __device__ __forceinline__ F2 fold_warps(M& sm, int buf, const float (*H)[S::C],
     }
     // The buffers take turns: a CTA sends into this one again only after it has had the next round from
     // everybody, who sent that after reading this one.
-    if (rounds.waiting) rounds.waiting = mbar_wait(arrived, rounds.n >> 1 & 1u, err);
+    if (rounds.waiting && !mbar_wait(arrived, rounds.n >> 1 & 1u, err)) {
+      rounds.waiting = false;
+      rounds.silent = true;
+    }
     ++rounds.n;
     __syncwarp();
     F2 h = state;   // entering the tile
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) rec_forward_kernel(RecArgs p
     };
     if (now) tile(Yes{}); else tile(No{});
   }
-  if (CLUSTER) cluster_barrier();   // nobody leaves while others may still write into its shared memory
+  if (CLUSTER) leave_cluster(rounds);
 }
 
 template <class S, bool TIED, bool CLUSTER>
@@ -749,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(RecArgs p) {
     };
     if (now) tile(Yes{}); else tile(No{});
   }
-  if (CLUSTER) cluster_barrier();
+  if (CLUSTER) leave_cluster(rounds);
 }
 
 // One token: 14 bytes an element in bf16 (x, f, out, and the fp32 state both ways), nothing else to wait
