@@ -69,6 +69,15 @@ __device__ __forceinline__ uint64_t wait_limit_ns(const ErrRec* rec) {
 }
 
 // ---------------------------------------------------------------------------------------
+// Host checks
+// ---------------------------------------------------------------------------------------
+// Whether two arguments' bytes meet (absent and empty ones meet nothing).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// ---------------------------------------------------------------------------------------
 // Element conversions
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {

@@ -50,3 +50,30 @@ def test_after_a_wait_ran_out_the_walk_ends(dtype, backward, cuda_device):
     for a, b in zip(call(), want):
         assert torch.equal(a, b)
     la.lightning_attn_check(ws)
+
+
+@pytest.mark.parametrize("T", [0, 3, 700])
+@pytest.mark.parametrize("by", [-1, 1, 3])
+def test_states_that_meet(T, by, cuda_device):
+    """state_out a few sequences behind or ahead of state_in in one buffer, dstate_in likewise: as apart."""
+    torch, la = _torch()
+    rng = np.random.default_rng(T + abs(by))
+    B, W = 40, 1000
+    x, f, d = _rand(rng, (B, T, W), "f32")[0], _gates(rng, (B, T, W), "f32")[0], _rand(rng, (B, T, W), "f32")[0]
+    ws = _ws(la, B, B * T, W, x, True)
+    buf = torch.empty(B + abs(by), W, device="cuda")
+    first, last = (buf[:B], buf[by:]) if by > 0 else (buf[-by:], buf[:B])
+    s = _rand(rng, (B, W), "f32")[0]
+    zero = torch.zeros(B, W, device="cuda")
+    for backward in (False, True):
+        got = []
+        for given, to in ((s, torch.empty_like(s)), (first.copy_(s), last)):
+            a, b = torch.empty_like(x), torch.empty_like(x)
+            if backward:
+                la.lightning_attn_gated_recurrence_backward(x, f, d, a, b, zero, given, to, workspace=ws)
+            else:
+                la.lightning_attn_gated_recurrence(x, f, a, given, to, workspace=ws)
+                b = a
+            got.append((a, b, to.clone()))
+        la.lightning_attn_check(ws)
+        assert all(torch.equal(a, b) for a, b in zip(*got))
