@@ -426,9 +426,11 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
  * where a sequence starts in the packed rows, and on the other arguments' sizes, by fp32
  * rounding only; it is the same for every call with the same arguments.
  *
- *   x, f, out    [B, T, W] dtype (x and f read only; out may not alias them).
+ *   x, f, out    [B, T, W] dtype (x and f read only).
  *   state_in     fp32 [B, W] initial state per sequence, or NULL for zeros.
- *   state_out    fp32 [B, W] final state, or NULL.  May be state_in (in place).
+ *   state_out    fp32 [B, W] final state, or NULL.  May be state_in (in place) or meet it.
+ *                Nothing else that a call writes may meet another argument's bytes
+ *                (LA_ERR_INVALID_ARG), here and in the calls below.
  *   checkpoints  fp32 [ceil(B*T / LA_RECURRENCE_CHECKPOINT_ROWS), W], or NULL: written with
  *                the fp32 state that each LA_RECURRENCE_CHECKPOINT_ROWS-th packed row starts
  *                from, for lightning_attn_gated_recurrence_backward.
@@ -471,7 +473,8 @@ LA_API la_status lightning_attn_gated_recurrence_varlen(const void* x, const voi
 
 /*
  * One token for each of B sequences: x, f, out [B, W]; state fp32 [B, W], updated IN PLACE.
- * Needs no workspace and allocates nothing.  Other arguments as above.
+ * Needs no workspace and allocates nothing.  Other arguments as above.  In fp32 state may be
+ * x, f or out itself.
  */
 LA_API la_status lightning_attn_gated_recurrence_step(const void* x, const void* f, void* out, float* state, int B,
                                                       int W, la_dtype dtype, la_input_mode input_mode,
@@ -486,10 +489,11 @@ LA_API la_status lightning_attn_gated_recurrence_step(const void* x, const void*
  * h is recomputed in fp32 block by block from `checkpoints`, so that the rounded out is
  * not needed and one tensor less is read.
  *   x, f         [B, T, W] dtype, the forward's inputs; dout [B, T, W] dtype.
- *   dx, df       [B, T, W] dtype, written (none may alias an input or the other).
+ *   dx, df       [B, T, W] dtype, written.
  *   state_in     fp32 [B, W], the forward's initial state, or NULL (zeros).
  *   dstate_out   fp32 [B, W], the gradient reaching the final state, or NULL (zeros).
- *   dstate_in    fp32 [B, W], written, or NULL.  May be dstate_out (in place).
+ *   dstate_in    fp32 [B, W], written, or NULL.  May be dstate_out (in place) or meet it, not
+ *                state_in.
  *   checkpoints  as the forward of the same x, f, state_in and input_mode wrote them, or
  *                NULL: they are recomputed (one more read of x and f).
  *   workspace    >= lightning_attn_gated_recurrence_workspace_size(..., backward = 1) bytes.

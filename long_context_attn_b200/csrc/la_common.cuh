@@ -76,6 +76,10 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && na && nb && x < y + nb && y < x + na;
 }
+// Whether they meet other than by being the same: what an element-wise operation cannot do in place.
+inline bool shifted(const void* a, size_t na, const void* b, size_t nb) {
+  return overlap(a, na, b, nb) && !(a == b && na == nb);
+}
 
 // ---------------------------------------------------------------------------------------
 // Element conversions

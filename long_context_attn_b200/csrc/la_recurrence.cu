@@ -947,17 +947,9 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
   // marks hold a sequence and two bits; offsets inside a tile are 32-bit
   if (p.tokens > INT32_MAX || p.nseq > (1 << 28) || p.W > (1 << 22)) return LA_ERR_UNSUPPORTED;
   if (p.tokens > 0) {
-    const void* in[3] = {p.x, p.f, p.dout};
-    void* out[2] = {backward ? p.dx : p.out, p.df};
-    const int nin = backward ? 3 : 2, nout = backward ? 2 : 1;
-    for (int i = 0; i < nin; ++i)
-      if (!in[i] || !aligned16(in[i])) return LA_ERR_INVALID_ARG;
-    for (int o = 0; o < nout; ++o) {
-      if (!out[o] || !aligned16(out[o])) return LA_ERR_INVALID_ARG;
-      for (int i = 0; i < nin; ++i)
-        if (out[o] == in[i]) return LA_ERR_INVALID_ARG;
-    }
-    if (backward && p.dx == p.df) return LA_ERR_INVALID_ARG;
+    for (const void* t : {p.x, p.f, static_cast<const void*>(backward ? p.dx : p.out)})
+      if (!t || !aligned16(t)) return LA_ERR_INVALID_ARG;
+    if (backward && (!p.dout || !aligned16(p.dout) || !p.df || !aligned16(p.df))) return LA_ERR_INVALID_ARG;
   }
   for (const void* s : {static_cast<const void*>(p.s0), static_cast<const void*>(p.s1),
                         static_cast<const void*>(p.ds0), static_cast<const void*>(p.ds1),
@@ -965,6 +957,23 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
     if (s && !aligned16(s)) return LA_ERR_INVALID_ARG;
   const RecLayout l = rec_layout(p.nseq, p.tokens, p.W, backward);
   if (!workspace || !aligned256(workspace) || ws_bytes < l.total) return LA_ERR_INVALID_ARG;
+  // Rows and sequences are worked on in any order, so nothing that is written may meet anything else; but the
+  // states the walk ends with may meet those it begins with, which are then read from a copy.
+  const size_t rows = static_cast<size_t>(p.tokens) * p.W * (dt == LA_BF16 ? 2 : 4);
+  const size_t states = sizeof(float) * static_cast<size_t>(p.nseq) * p.W;
+  const size_t cks = sizeof(float) * static_cast<size_t>((p.tokens + kCkRows - 1) / kCkRows) * p.W;
+  enum { kNever, kBegin, kEndOfWalk };
+  const struct { const void* at; size_t bytes; bool written; int walk; } args[] = {
+      {p.x, rows, false, kNever}, {p.f, rows, false, kNever}, {p.dout, rows, false, kNever},
+      {p.cu, sizeof(int) * (static_cast<size_t>(p.nseq) + 1), false, kNever},
+      {p.s0, states, false, backward ? kNever : kBegin}, {p.s1, states, true, kEndOfWalk},
+      {p.ds1, states, false, kBegin}, {p.ds0, states, true, kEndOfWalk}, {p.ck, cks, !backward, kNever},
+      {p.out, rows, true, kNever}, {p.dx, rows, true, kNever}, {p.df, rows, true, kNever},
+      {workspace, l.total, true, kNever}};
+  for (const auto& w : args)
+    for (const auto& t : args)
+      if (w.written && &t != &w && !(w.walk == kEndOfWalk && t.walk == kBegin) && overlap(w.at, w.bytes, t.at, t.bytes))
+        return LA_ERR_INVALID_ARG;
   p.err = static_cast<ErrRec*>(workspace);
   p.tied = mode == LA_INPUT_TIED;
   cudaError_t e = cudaSuccess;
@@ -1055,10 +1064,13 @@ la_status lightning_attn_gated_recurrence_step(const void* x, const void* f, voi
     return LA_ERR_INVALID_ARG;
   for (const void* t : {x, f, static_cast<const void*>(out), static_cast<const void*>(state)})
     if (!t || !la::aligned16(t)) return LA_ERR_INVALID_ARG;
-  if (out == x || out == f) return LA_ERR_INVALID_ARG;
   // the elements are independent: whole 16-byte vectors of the flat array where it is made of them
   const int64_t n = static_cast<int64_t>(B) * W;
   if (n > (int64_t(1) << 38)) return LA_ERR_UNSUPPORTED;
+  const size_t row_bytes = static_cast<size_t>(n) * (dtype == LA_BF16 ? 2 : 4), state_bytes = static_cast<size_t>(n) * 4;
+  for (const void* t : {x, f})
+    if (la::overlap(out, row_bytes, t, row_bytes) || la::shifted(state, state_bytes, t, row_bytes)) return LA_ERR_INVALID_ARG;
+  if (la::shifted(state, state_bytes, out, row_bytes)) return LA_ERR_INVALID_ARG;
   const int tied = input_mode == LA_INPUT_TIED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =

@@ -135,6 +135,79 @@ def test_recurrence_workspace_size(lib):
     assert f(1, 0, 64, 0, 0) >= 256
 
 
+def _walks(lib):
+    """The four calls over rows as functions of keywords, with arguments that do not meet by default."""
+    vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    p = _ptrs(16)
+
+    def walk(name, packed, backward):
+        fn = getattr(lib, "lightning_attn_gated_recurrence" + ("_backward" if backward else "") + ("_varlen" if packed else ""))
+        fn.argtypes = [vp] * ((9 if backward else 6) + packed) + [i32] * 5 + [vp, sz, vp]
+
+        def call(**kw):
+            a = dict(x=p[0], f=p[1], dout=p[2], out=p[3], df=p[4], s0=p[6], s1=p[7], ds1=p[8], ds0=p[9], ck=p[10], cu=p[5],
+                     ws=WS)
+            a.update(kw)
+            states = ("s0", "ds1", "ds0") if backward else ("s0", "s1")
+            head = ("x", "f", *(("dout", "out", "df") if backward else ("out",)), *states, "ck", *(("cu",) if packed else ()))
+            return fn(*(a[k] for k in head), 2, kw.get("T", 8), 64, 1, 1, a["ws"], 1 << 40, None)
+        return call
+    return [(walk("", packed, backward), packed, backward) for packed in (0, 1) for backward in (0, 1)]
+
+
+def test_recurrence_entries_refuse_overlaps(lib):
+    """Rows are 8 * 64 bf16 values (twice that for two sequences of 8), states 2 * 64 floats; a buffer that starts inside
+    another one, or ends inside it, meets it."""
+    near = lambda q, by: ctypes.c_void_p(q.value + by)  # noqa: E731
+    p = _ptrs(16)
+    for call, packed, backward in _walks(lib):
+        rows = 1024 if packed else 2048
+        written = ["out", "df"] if backward else ["out"]
+        others = ["x", "f"] + (["dout"] if backward else []) + written
+        at = dict(x=p[0], f=p[1], dout=p[2], out=p[3], df=p[4], s0=p[6], s1=p[7], ds1=p[8], ds0=p[9], ck=p[10], cu=p[5])
+        bad = [{w: near(at[o], by)} for w in written for o in others if o != w for by in (0, 16, -16, rows - 16, 16 - rows)]
+        bad += [{w: near(at[o], by)} for w in written for o in ["s0", "ck"] + ["cu"] * packed for by in (0, -16)]
+        bad += [dict(ck=near(at["x"], 16))] if not backward else []
+        last = "ds0" if backward else "s1"
+        bad += [{last: near(at[o], by)} for o in others + ["ck"] for by in (0, 16, -16)]
+        bad += [dict(out=WS), {last: near(WS, 256)}]
+        if backward:
+            bad += [dict(ds0=near(at["s0"], by)) for by in (0, 16, -256)]
+            bad += [dict(s0=at["ds1"], ds0=at["ds1"])]
+        for kw in bad:
+            assert call(**kw) == 1, (packed, backward, kw)
+        # what may be: the final states over the initial ones, and buffers side by side (3: accepted, but there is no
+        # GPU; where there is one, these addresses are not to reach it)
+        if torch.cuda.is_available():
+            continue
+        first = at["ds1" if backward else "s0"]
+        for kw in ({}, {last: first}, {last: near(first, 16)}, {last: near(first, -256)}, dict(out=near(at["x"], rows)),
+                   dict(out=near(at["x"], -rows)), dict(x=at["f"])):
+            assert call(**kw) == 3, (packed, backward, kw)
+
+
+def test_recurrence_step_refuses_overlaps(lib):
+    vp, i32 = ctypes.c_void_p, ctypes.c_int
+    step = lib.lightning_attn_gated_recurrence_step
+    step.argtypes = [vp] * 4 + [i32] * 4 + [vp]
+    p = _ptrs(4)
+    near = lambda q, by: vp(q.value + by)  # noqa: E731
+
+    def call(x=p[0], f=p[1], out=p[2], state=p[3], dt=1):
+        return step(x, f, out, state, 2, 64, dt, 1, None)
+
+    for dt, row in ((0, 512), (1, 256)):
+        for by in (0, 16, -16, row - 16, 16 - row):
+            assert call(out=near(p[0], by), dt=dt) == 1 and call(out=near(p[1], by), dt=dt) == 1
+        for by in (16, -16, row - 16, -496):
+            assert call(state=near(p[0], by), dt=dt) == 1 and call(state=near(p[2], by), dt=dt) == 1
+    assert call(state=p[0]) == 1 and call(state=p[2]) == 1      # bf16 values under fp32 ones
+    if torch.cuda.is_available():       # accepted calls' addresses are not to reach a GPU
+        return
+    for kw in ({}, dict(state=p[0], dt=0), dict(state=p[2], dt=0), dict(out=near(p[0], 256)), dict(state=near(p[0], -512))):
+        assert call(**kw) == 3, kw
+
+
 def test_layer_norm_entries_refuse(lib):
     vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     fwd, bwd = lib.lightning_attn_layer_norm, lib.lightning_attn_layer_norm_backward
