@@ -531,7 +531,9 @@ LA_API size_t lightning_attn_gated_recurrence_workspace_size(int num_seqs, int t
  *   x, out       [rows, W] dtype; out may be x or residual (in place).
  *   residual     [rows, W] dtype, or NULL (s = x).
  *   sum_out      [rows, W] dtype, or NULL: s, rounded to dtype (the residual stream that goes
- *                on).  May be x or residual (in place), not out.
+ *                on).  May be x or residual (in place), not out.  What a call writes may not
+ *                meet another argument's bytes in any other way (LA_ERR_INVALID_ARG), here and
+ *                in the backward.
  *   weight, bias fp32 [W], or NULL (ones, zeros).
  *   W            1 <= W <= 16384 (beyond: LA_ERR_UNSUPPORTED); rows >= 0; eps > 0.  Rows whose
  *                bytes are a multiple of 16 are read as 16-byte vectors, others element by
@@ -550,7 +552,8 @@ LA_API la_status lightning_attn_layer_norm(const void* x, const void* residual, 
  *   dout         [rows, W] dtype.
  *   dsum         [rows, W] dtype, the gradient reaching sum_out, or NULL.
  *   dx           [rows, W] dtype, written; may be s, dout or dsum (in place).
- *   dweight, dbias  fp32 [W], written (zeros for rows == 0), or NULL.
+ *   dweight, dbias  fp32 [W], written (zeros for rows == 0), or NULL.  Written after everything
+ *                else has been read: they may lie where s, dout, dsum or weight does.
  *   workspace    needed iff dweight or dbias is given: >= lightning_attn_layer_norm_workspace_size
  *                bytes, 256-byte aligned.
  * Other arguments as the forward.

@@ -544,6 +544,8 @@ size_t ln_ws_bytes(int rows, int W) {
   return n < 256 ? 256 : (n + 255) & ~size_t(255);
 }
 
+size_t ln_bytes(int rows, int W, la_dtype dt) { return static_cast<size_t>(rows) * W * (dt == LA_BF16 ? 2 : 4); }
+
 bool ln_valid(int rows, int W, la_dtype dt, float eps, const float* w, const float* b) {
   return rows >= 0 && W >= 1 && (dt == LA_F32 || dt == LA_BF16) && eps > 0.0f && (!w || aligned16(w)) &&
          (!b || aligned16(b));
@@ -561,8 +563,15 @@ la_status lightning_attn_layer_norm(const void* x, const void* residual, const f
   if (W > la::kMaxNormWidth) return LA_ERR_UNSUPPORTED;
   if (rows == 0) return LA_OK;
   if (!x || !out || !la::aligned16(x) || !la::aligned16(out) || (residual && !la::aligned16(residual)) ||
-      (sum_out && (!la::aligned16(sum_out) || sum_out == out)))
+      (sum_out && !la::aligned16(sum_out)))
     return LA_ERR_INVALID_ARG;
+  // rows are written while others are still to be read: in place or apart, nothing between
+  const size_t n = la::ln_bytes(rows, W, dtype), nw = sizeof(float) * W;
+  if (la::overlap(out, n, sum_out, n)) return LA_ERR_INVALID_ARG;
+  for (const void* to : {static_cast<const void*>(out), static_cast<const void*>(sum_out)})
+    if (la::shifted(to, n, x, n) || la::shifted(to, n, residual, n) || la::overlap(to, n, weight, nw) ||
+        la::overlap(to, n, bias, nw))
+      return LA_ERR_INVALID_ARG;
   la::LnArgs a{};
   a.x = x; a.residual = residual; a.w = weight; a.b = bias; a.out = out; a.sum_out = sum_out;
   a.rows = rows; a.W = W; a.eps = eps; a.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -574,7 +583,8 @@ la_status lightning_attn_layer_norm_backward(const void* s, const void* dout, co
                                              float eps, void* workspace, size_t workspace_bytes, la_stream_t stream) {
   if (!la::ln_valid(rows, W, dtype, eps, weight, nullptr)) return LA_ERR_INVALID_ARG;
   if (W > la::kMaxNormWidth) return LA_ERR_UNSUPPORTED;
-  if ((dweight && !la::aligned16(dweight)) || (dbias && !la::aligned16(dbias)) || (dweight && dweight == dbias))
+  const size_t nw = sizeof(float) * W;
+  if ((dweight && !la::aligned16(dweight)) || (dbias && !la::aligned16(dbias)) || la::overlap(dweight, nw, dbias, nw))
     return LA_ERR_INVALID_ARG;
   const bool sums = dweight || dbias;
   if (sums && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
@@ -589,6 +599,14 @@ la_status lightning_attn_layer_norm_backward(const void* s, const void* dout, co
   if (!s || !dout || !dx || !la::aligned16(s) || !la::aligned16(dout) || !la::aligned16(dx) ||
       (dsum && !la::aligned16(dsum)))
     return LA_ERR_INVALID_ARG;
+  const size_t n = la::ln_bytes(rows, W, dtype), parts = sums ? la::ln_ws_bytes(rows, W) : 0;
+  if (la::shifted(dx, n, s, n) || la::shifted(dx, n, dout, n) || la::shifted(dx, n, dsum, n) ||
+      la::overlap(dx, n, weight, nw) || la::overlap(dx, n, dweight, nw) || la::overlap(dx, n, dbias, nw))
+    return LA_ERR_INVALID_ARG;
+  for (const void* t : {s, dout, dsum, static_cast<const void*>(dx)})
+    if (la::overlap(workspace, parts, t, n)) return LA_ERR_INVALID_ARG;
+  for (const void* t : {weight, static_cast<const float*>(dweight), static_cast<const float*>(dbias)})
+    if (la::overlap(workspace, parts, t, nw)) return LA_ERR_INVALID_ARG;
   la::LnArgs a{};
   a.x = s; a.dout = dout; a.dsum = dsum; a.w = weight; a.out = dx; a.dw = dweight; a.db = dbias;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;

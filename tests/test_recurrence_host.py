@@ -243,6 +243,46 @@ def test_layer_norm_entries_refuse(lib):
     assert size(0, 64) >= 256 and size(100, 64) >= 2 * 64 * 4
 
 
+def test_layer_norm_entries_refuse_overlaps(lib):
+    """4 rows of 64 bf16 values: 512 bytes; the weights are 256 bytes."""
+    vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    fwd, bwd = lib.lightning_attn_layer_norm, lib.lightning_attn_layer_norm_backward
+    fwd.argtypes = [vp] * 6 + [i32] * 3 + [f32, vp]
+    bwd.argtypes = [vp] * 7 + [i32] * 3 + [f32, vp, sz, vp]
+    p = _ptrs(8)
+    near = lambda q, by: vp(q.value + by)  # noqa: E731
+    at = dict(x=p[0], res=p[1], w=p[2], b=p[3], out=p[4], sum=p[5])
+    grad = dict(s=p[0], dout=p[1], dsum=p[2], w=p[3], dx=p[4], dw=p[5], db=p[6], ws=WS)
+
+    def f(**kw):
+        a = {**at, **kw}
+        return fwd(a["x"], a["res"], a["w"], a["b"], a["out"], a["sum"], 4, 64, 1, 1e-5, None)
+
+    def g(**kw):
+        a = {**grad, **kw}
+        return bwd(a["s"], a["dout"], a["dsum"], a["w"], a["dx"], a["dw"], a["db"], 4, 64, 1, 1e-5, a["ws"], 1 << 30, None)
+
+    off = (16, -16, 496, -496)
+    bad = [{to: near(at[o], by)} for to in ("out", "sum") for o in ("x", "res") for by in off]
+    bad += [{to: near(at[o], by)} for to in ("out", "sum") for o in ("w", "b") for by in (0, 16, -496, 240)]
+    bad += [dict(sum=near(at["out"], by)) for by in (0, *off)]
+    for kw in bad:
+        assert f(**kw) == 1, kw
+    bad_g = [dict(dx=near(grad[o], by)) for o in ("s", "dout", "dsum") for by in off]
+    bad_g += [dict(dx=near(grad[o], by)) for o in ("w", "dw", "db", "ws") for by in (0, 16)]
+    bad_g += [dict(dw=near(grad["db"], by)) for by in (0, 16, -240)] + [{k: WS} for k in ("s", "dout", "dsum", "w", "dw", "db")]
+    for kw in bad_g:
+        assert g(**kw) == 1, kw
+    if torch.cuda.is_available():       # accepted calls' addresses are not to reach a GPU
+        return
+    for kw in ({}, dict(out=p[0]), dict(out=p[1]), dict(sum=p[0]), dict(out=p[0], sum=p[1]), dict(out=near(p[0], 512)),
+               dict(res=p[0]), dict(b=p[2])):
+        assert f(**kw) == 3, kw
+    for kw in ({}, dict(dx=p[0]), dict(dx=p[1]), dict(dx=p[2]), dict(dw=p[3]), dict(dw=p[1]), dict(dx=near(p[0], -512)),
+               dict(db=None)):
+        assert g(**kw) == 3, kw
+
+
 # --------------------------------------------------------------------------- binding
 def test_binding_refuses_host_tensors(lib):
     from long_context_attn_b200 import lightning_attn as la
