@@ -215,19 +215,28 @@ def lightning_attention_sequence_parallel(q, k, v, g=None, state0=None, norm_wei
                                                      phi, mode, eps)
 
 
+def _aligned(t):
+    """t as the library takes it: contiguous, from a 16-byte boundary (a slice may start anywhere, and so may
+    the gradients that torch.cat and split hand back).  A copy only where it is not."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _GatedRecurrence(torch.autograd.Function):
     """x, f [B, T, W] (cu_seqlens None) or packed [total, W]."""
 
     @staticmethod
     def forward(ctx, x, f, state_in, cu_seqlens, input_mode):
         ctx.set_materialize_grads(False)
-        x, f = x.contiguous(), f.contiguous()
+        x, f, cu_seqlens = _aligned(x), _aligned(f), _aligned(cu_seqlens)
         W = x.shape[-1]
         tokens = x.shape[0] if cu_seqlens is not None else x.shape[0] * x.shape[1]
         n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
         out = torch.empty_like(x)
         state_out = torch.empty((n, W), dtype=torch.float32, device=x.device)
-        s_in = None if state_in is None else state_in.detach().contiguous()
+        s_in = None if state_in is None else _aligned(state_in.detach())
         saved = la.new_recurrence_checkpoints(tokens, W, x.device) if any(ctx.needs_input_grad) else None
         ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x)), x.device)
         if cu_seqlens is None:
@@ -244,8 +253,8 @@ class _GatedRecurrence(torch.autograd.Function):
         x, f, s_in, cu, saved = ctx.saved_tensors
         n, tokens, input_mode = ctx.cfg
         W = x.shape[-1]
-        dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype).contiguous()
-        ds_out = None if dstate_out is None else dstate_out.float().contiguous()
+        dout = torch.zeros_like(x) if dout is None else _aligned(dout.to(x.dtype))
+        ds_out = None if dstate_out is None else _aligned(dstate_out.float())
         dx, df = torch.empty_like(x), torch.empty_like(f)
         ds_in = torch.empty((n, W), dtype=torch.float32, device=x.device) if ctx.needs_input_grad[2] else None
         ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x), True),
@@ -275,13 +284,11 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps):
         ctx.set_materialize_grads(False)
-        x = x.contiguous()
-        residual = None if residual is None else residual.contiguous()
-        weight = None if weight is None else weight.detach()
+        x, residual = _aligned(x), _aligned(residual)
+        weight, bias = (None if t is None else _aligned(t.detach()) for t in (weight, bias))
         out = torch.empty_like(x)
         s = None if residual is None else torch.empty_like(x)
-        la.lightning_attn_layer_norm(x, out, residual=residual, sum_out=s, weight=weight,
-                                     bias=None if bias is None else bias.detach(), eps=eps)
+        la.lightning_attn_layer_norm(x, out, residual=residual, sum_out=s, weight=weight, bias=bias, eps=eps)
         ctx.save_for_backward(x if s is None else s, weight)
         ctx.eps = eps
         return out if s is None else (out, s)
@@ -292,8 +299,8 @@ class _LayerNorm(torch.autograd.Function):
         s, weight = ctx.saved_tensors
         W = s.shape[-1]
         need = ctx.needs_input_grad
-        dout = torch.zeros_like(s) if dout is None else dout.to(s.dtype).contiguous()
-        dsum = None if dsum is None else dsum.to(s.dtype).contiguous()
+        dout = torch.zeros_like(s) if dout is None else _aligned(dout.to(s.dtype))
+        dsum = None if dsum is None else _aligned(dsum.to(s.dtype))
         dx = torch.empty_like(s)
         dw, db = (torch.empty(W, dtype=torch.float32, device=s.device) if n else None for n in need[1:3])
         ws = None

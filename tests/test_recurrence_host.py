@@ -450,3 +450,73 @@ def test_layer_norm_autograd_without_residual_or_weights(ag):
     got, = torch.autograd.grad((y * d).sum(), x)
     want, = torch.autograd.grad((torch.nn.functional.layer_norm(x, (6,)) * d).sum(), x)
     torch.testing.assert_close(got, want, rtol=1e-4, atol=1e-5)
+
+
+class _StrictRecorder(_Recorder):
+    """Refuses what the library refuses: tensors that are not contiguous, or not from a 16-byte boundary."""
+
+    def __getattribute__(self, name):
+        fn = super().__getattribute__(name)
+        if not name.startswith("lightning_attn_") or name.endswith("_size"):
+            return fn
+
+        def call(*args, **kw):
+            for t in (*args, *kw.values()):
+                if torch.is_tensor(t):
+                    assert t.is_contiguous() and t.data_ptr() % 16 == 0, (name, t.shape, t.data_ptr() % 16)
+            return fn(*args, **kw)
+        return call
+
+
+@pytest.fixture
+def strict(monkeypatch):
+    from long_context_attn_b200 import autograd
+    fake = _StrictRecorder()
+    monkeypatch.setattr(autograd, "la", fake)
+    autograd.fake = fake
+    return autograd
+
+
+@pytest.mark.parametrize("W", [7, 25, 100])
+@pytest.mark.parametrize("packed", [False, True])
+def test_recurrence_autograd_takes_views(strict, packed, W):
+    """Slices that start off a 16-byte boundary, for every input, and such gradients (torch.cat's of parts with an odd
+    number of rows): as torch's own autograd."""
+    rng = np.random.default_rng(W)
+    rows, lens = 5, ([2, 3] if packed else [5])
+    xs, fs, ss = _leaf(rng, 1 + rows, W), _leaf(rng, 1 + rows, W), _leaf(rng, 1 + len(lens), W)
+    wo, ws = torch.randn(3 + rows, W), torch.randn(1 + len(lens), W)
+
+    def loss(run):
+        x, f, s = xs[1:], fs[1:], ss[1:]
+        out, st = run(x, f, s)
+        return (torch.cat((torch.tanh(xs[:3]), out)) * wo).sum() + (torch.cat((ss[:1], st)) * ws).sum()
+
+    def ours(x, f, s):
+        if packed:
+            cu = torch.tensor([-1, 0, 2, 5], dtype=torch.int32)[1:]
+            return strict.gated_recurrence_varlen(x, f, cu, s, input_mode=strict.fake.LA_INPUT_PLAIN)
+        out, st = strict.gated_recurrence(x[None], f[None], s, input_mode=strict.fake.LA_INPUT_PLAIN)
+        return out[0], st
+
+    got = torch.autograd.grad(loss(ours), (xs, fs, ss))
+    want = torch.autograd.grad(loss(lambda x, f, s: _plain_recurrence(x, f, lens, False, s)), (xs, fs, ss))
+    for g, w in zip(got, want):
+        torch.testing.assert_close(g, w, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("W", [7, 25, 100])
+def test_layer_norm_autograd_takes_views(strict, W):
+    rng = np.random.default_rng(W)
+    xs, rs, wb = _leaf(rng, 6, W), _leaf(rng, 6, W), _leaf(rng, 1 + 2 * W)
+    wo, ws = torch.randn(8, W), torch.randn(8, W)
+
+    def loss(run):
+        out, s = run(xs[1:], wb[1:1 + W], wb[1 + W:], rs[1:])
+        return (torch.cat((xs[:3], out)) * wo).sum() + (torch.cat((rs[:3], s)) * ws).sum()
+
+    got = torch.autograd.grad(loss(lambda x, w, b, r: strict.layer_norm(x, w, b, residual=r)), (xs, rs, wb))
+    want = torch.autograd.grad(loss(lambda x, w, b, r: (torch.nn.functional.layer_norm(x + r, (W,), w, b, 1e-5), x + r)),
+                               (xs, rs, wb))
+    for g, w in zip(got, want):
+        torch.testing.assert_close(g, w, rtol=1e-4, atol=1e-5)
