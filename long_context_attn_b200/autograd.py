@@ -228,7 +228,7 @@ class _GatedRecurrence(torch.autograd.Function):
     """x, f [B, T, W] (cu_seqlens None) or packed [total, W]."""
 
     @staticmethod
-    def forward(ctx, x, f, state_in, cu_seqlens, input_mode):
+    def forward(ctx, x, f, state_in, cu_seqlens, input_mode, workspace):
         ctx.set_materialize_grads(False)
         x, f, cu_seqlens = _aligned(x), _aligned(f), _aligned(cu_seqlens)
         W = x.shape[-1]
@@ -238,46 +238,53 @@ class _GatedRecurrence(torch.autograd.Function):
         state_out = torch.empty((n, W), dtype=torch.float32, device=x.device)
         s_in = None if state_in is None else _aligned(state_in.detach())
         saved = la.new_recurrence_checkpoints(tokens, W, x.device) if any(ctx.needs_input_grad) else None
-        ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x)), x.device)
+        ws = workspace
+        if ws is None:
+            ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x)), x.device)
         if cu_seqlens is None:
             la.lightning_attn_gated_recurrence(x, f, out, s_in, state_out, saved, input_mode, ws)
         else:
             la.lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, s_in, state_out, saved, input_mode, ws)
         ctx.save_for_backward(x, f, s_in, cu_seqlens, saved)
-        ctx.cfg = (n, tokens, input_mode)
+        ctx.cfg = (n, tokens, input_mode, workspace)
         return out, state_out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout, dstate_out):
         x, f, s_in, cu, saved = ctx.saved_tensors
-        n, tokens, input_mode = ctx.cfg
+        n, tokens, input_mode, ws = ctx.cfg
         W = x.shape[-1]
         dout = torch.zeros_like(x) if dout is None else _aligned(dout.to(x.dtype))
         ds_out = None if dstate_out is None else _aligned(dstate_out.float())
         dx, df = torch.empty_like(x), torch.empty_like(f)
         ds_in = torch.empty((n, W), dtype=torch.float32, device=x.device) if ctx.needs_input_grad[2] else None
-        ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x), True),
-                              x.device)
+        if ws is None:
+            ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(n, tokens, W, la._dtype(x), True),
+                                  x.device)
         if cu is None:
             la.lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, s_in, ds_out, ds_in, saved, input_mode, ws)
         else:
             la.lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu, s_in, ds_out, ds_in, saved,
                                                                input_mode, ws)
-        return dx, df, ds_in, None, None
+        return dx, df, ds_in, None, None, None
 
 
-def gated_recurrence(x, f, state_in=None, input_mode: int = la.LA_INPUT_TIED):
+def gated_recurrence(x, f, state_in=None, input_mode: int = la.LA_INPUT_TIED, workspace=None):
     """Differentiable gated recurrence h_t = a_t h_{t-1} + b_t, a = sigmoid(f), b = x or (1 - a) x:
-    x, f [B, T, W]; state_in fp32 [B, W] or None.  Returns (out [B, T, W], state_out fp32 [B, W])."""
-    return _GatedRecurrence.apply(x, f, state_in, None, input_mode)
+    x, f [B, T, W]; state_in fp32 [B, W] or None.  Returns (out [B, T, W], state_out fp32 [B, W]).
+    Failures found on the device (malformed cu_seqlens, a wait that ran out) are recorded in
+    `workspace`, the caller's, where lightning_attn_check finds them after the forward and after the
+    backward: from new_workspace, lightning_attn_gated_recurrence_workspace_size(..., backward=True)
+    bytes.  Without one, each call makes its own and the record is lost with it."""
+    return _GatedRecurrence.apply(x, f, state_in, None, input_mode, workspace)
 
 
-def gated_recurrence_varlen(x, f, cu_seqlens, state_in=None, input_mode: int = la.LA_INPUT_TIED):
+def gated_recurrence_varlen(x, f, cu_seqlens, state_in=None, input_mode: int = la.LA_INPUT_TIED, workspace=None):
     """Differentiable gated recurrence over packed sequences: x, f [total, W]; cu_seqlens int32
-    device [N + 1] with cu_seqlens[N] == total; state_in fp32 [N, W] or None.  Returns
-    (out [total, W], state_out fp32 [N, W])."""
-    return _GatedRecurrence.apply(x, f, state_in, cu_seqlens, input_mode)
+    device [N + 1] with cu_seqlens[N] == total; state_in fp32 [N, W] or None; workspace as for
+    gated_recurrence.  Returns (out [total, W], state_out fp32 [N, W])."""
+    return _GatedRecurrence.apply(x, f, state_in, cu_seqlens, input_mode, workspace)
 
 
 class _LayerNorm(torch.autograd.Function):

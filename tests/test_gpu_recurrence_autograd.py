@@ -68,3 +68,22 @@ def test_layer_norm_of_views(W, dtype, cuda_device):
         ref.check("dx", _np(t.grad[1:]), q["dx"], q["dx_tol"], dtype)
     ref.check("dweight", _np(wb.grad[1:1 + W]), q["dweight"], q["dweight_tol"])
     ref.check("dbias", _np(wb.grad[1 + W:]), q["dbias"], q["dbias_tol"])
+
+
+def test_malformed_offsets_are_found_in_the_callers_workspace(cuda_device):
+    """After the forward and after the backward, each for itself; a good call then leaves the record clean."""
+    torch, la = _torch()
+    from long_context_attn_b200.autograd import gated_recurrence_varlen
+    rows, W = 300, 64
+    x = torch.randn(rows, W, device="cuda", requires_grad=True)
+    ws = la.new_workspace(la.lightning_attn_gated_recurrence_workspace_size(3, rows, W, la.LA_F32, True))
+    for cu, good in (([0, 200, 100, 300], False), ([0, 100, 200, 301], False), ([0, 100, 200, 300], True)):
+        out, _ = gated_recurrence_varlen(x, x, torch.tensor(cu, dtype=torch.int32, device="cuda"), workspace=ws)
+        for part in (lambda: None, out.sum().backward):
+            part()
+            if good:
+                la.lightning_attn_check(ws)
+                continue
+            with pytest.raises(la.LightningAttnError) as err:
+                la.lightning_attn_check(ws)
+            assert err.value.status == la.LA_ERR_DEVICE

@@ -520,3 +520,25 @@ def test_layer_norm_autograd_takes_views(strict, W):
                                (xs, rs, wb))
     for g, w in zip(got, want):
         torch.testing.assert_close(g, w, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_recurrence_autograd_uses_the_callers_workspace(ag, packed, monkeypatch):
+    """The error record of the forward and of the backward is where the caller can read it."""
+    seen = []
+
+    def note(name):
+        real = getattr(ag.fake, name)
+        monkeypatch.setattr(ag.fake, name, lambda *a: (seen.append(a[-1]), real(*a))[1])
+
+    tail = "_varlen" if packed else ""
+    note("lightning_attn_gated_recurrence" + tail)
+    note("lightning_attn_gated_recurrence_backward" + tail)
+    x, ws = torch.zeros(1, 4, 2, requires_grad=True), torch.zeros(4096, dtype=torch.uint8)
+    for given in (ws, None):
+        if packed:
+            out, _ = ag.gated_recurrence_varlen(x[0], x[0], torch.tensor([0, 4], dtype=torch.int32), workspace=given)
+        else:
+            out, _ = ag.gated_recurrence(x, x, workspace=given)
+        out.sum().backward()
+    assert len(seen) == 4 and all(w is ws for w in seen[:2]) and all(w is not ws and w is not None for w in seen[2:])
