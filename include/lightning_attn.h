@@ -527,7 +527,9 @@ LA_API size_t lightning_attn_gated_recurrence_workspace_size(int num_seqs, int t
  * norm with a mean and a bias that a layer's input passes.
  *   s = x + residual,   y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias,
  * var the mean of the squared deviations.  Sums are fp32; the deviations are taken from the
- * mean before they are squared; y comes from the unrounded s.
+ * rounded mean before they are squared, and their own mean is taken off again, so the error
+ * goes by the deviations' size, not by the values' (rows of equal values give the bias); y
+ * comes from the unrounded s.
  *   x, out       [rows, W] dtype; out may be x or residual (in place).
  *   residual     [rows, W] dtype, or NULL (s = x).
  *   sum_out      [rows, W] dtype, or NULL: s, rounded to dtype (the residual stream that goes

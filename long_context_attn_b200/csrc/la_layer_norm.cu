@@ -74,41 +74,37 @@ template <int V> __device__ __forceinline__ void load_w(const float* p, int c, f
   }
 }
 
-// Sums over the G threads of a row, in every one of them, in a fixed order.  `red` alternates between
-// calls, so one barrier a call is enough.
-using Sums = float4[2][32];
-template <int G> __device__ __forceinline__ float row_sum(float a, Sums& red, int& half) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (G == 32) return a;
-  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5].x = a;
-  __syncthreads();
-  a = red[half][threadIdx.x % (G / 32)].x;   // every warp adds the warps' sums for itself
-#pragma unroll
-  for (int o = G / 64; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  half ^= 1;
-  return a;
+// N sums over the G threads of a row, in every one of them, in a fixed order.  A warp's lanes divide the sums among
+// them, the half of a pair going on with one of it (6 shuffles for four sums, not 20), and so do the lanes that add the
+// warps'.  `red` alternates between calls, so one barrier a call is enough.
+using Sums = float[2][4][32];
+__device__ __forceinline__ float divide_sums(float lower, float upper, int lanes) {
+  const bool up = threadIdx.x & lanes;
+  const float mine = up ? upper : lower, other = up ? lower : upper;
+  return mine + __shfl_xor_sync(0xffffffffu, other, lanes);
 }
-template <int G> __device__ __forceinline__ float3 row_sum(float3 v, Sums& red, int& half) {
+template <int G, int N> __device__ __forceinline__ void row_sums(float (&v)[N], Sums& red, int& half) {
+  static_assert(N == 1 || N == 2 || N == 4, "the lanes are divided by halves");
+  constexpr int L = 32 / N;   // lanes a sum
+  const int lane = threadIdx.x & 31;
+  float a = v[0];
+  if constexpr (N == 2) a = divide_sums(v[0], v[1], 16);
+  if constexpr (N == 4) a = divide_sums(divide_sums(v[0], v[2], 16), divide_sums(v[1], v[3], 16), 8);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
-  }
-  if (G == 32) return v;
-  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5] = make_float4(v.x, v.y, v.z, 0.f);
-  __syncthreads();
-  const float4 t = red[half][threadIdx.x % (G / 32)];
-  v = make_float3(t.x, t.y, t.z);
+  for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if constexpr (G > 32) {
+    constexpr int NW = G / 32, S = NW < L ? NW : L;
+    if (lane % L == 0) red[half][lane / L][threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = red[half][lane / L][lane % S];
 #pragma unroll
-  for (int o = G / 64; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    for (int i = S; i < NW; i += S) a += red[half][lane / L][lane % S + i];
+#pragma unroll
+    for (int o = S / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    half ^= 1;
   }
-  half ^= 1;
-  return v;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = N == 1 ? a : __shfl_sync(0xffffffffu, a, k * L);
 }
 __device__ __forceinline__ float both(F2 a) {
   const float2 v = split(a);
@@ -124,19 +120,23 @@ template <typename T_, int V_, int NV_, int G_, bool FULL_> struct Row {
   __device__ __forceinline__ static bool in(int lane, int i, int W) { return FULL || column(lane, i) < W; }
 };
 
-// A row held in registers becomes its deviations from its mean; returns the sum of their squares over
-// the thread's own.
+// A row held in registers becomes its deviations from a first mean, which is rounded: a sum of W values is off by
+// up to 42 roundings of their size (32 of a thread's, 5 of a warp's, 5 of the warps').  8192 values of 1745.394 come out a
+// last place beside their mean, and over sqrt(eps) = 0.0032 that is 0.077 in z, which should be 0.  So the
+// mean of the deviations, `shift`, is taken off as well: their sum travels with that of their squares, and the variance is
+// the squares' mean less shift^2.  What is left are 42 roundings of the deviations' size.
 template <class R>
-__device__ __forceinline__ float center(F2 (*v)[R::U], int W, int lane, Sums& red, int& half) {
+__device__ __forceinline__ void center(F2 (*v)[R::U], int W, int lane, Sums& red, int& half, float& sum, float& squares) {
   F2 a = splat(0.f);
 #pragma unroll
   for (int i = 0; i < R::NV; ++i)
 #pragma unroll
     for (int e = 0; e < R::U; ++e) a = add2(a, v[i][e]);
-  // divided, not multiplied by 1 / W: the mean of equal values is then that value
-  const float mean = row_sum<R::G>(both(a), red, half) / static_cast<float>(W);
+  float total[1] = {both(a)};
+  row_sums<R::G>(total, red, half);
+  const float mean = total[0] / static_cast<float>(W);
   const F2 minus = R::V == 1 ? make_f2(-mean, 0.f) : splat(-mean);
-  F2 q = splat(0.f);
+  F2 q = splat(0.f), d = splat(0.f);
 #pragma unroll
   for (int i = 0; i < R::NV; ++i) {
     const bool in = R::in(lane, i, W);
@@ -144,13 +144,19 @@ __device__ __forceinline__ float center(F2 (*v)[R::U], int W, int lane, Sums& re
     for (int e = 0; e < R::U; ++e) {
       v[i][e] = add2(v[i][e], minus);
       if (!in) v[i][e] = splat(0.f);
+      d = add2(d, v[i][e]);
       q = fma2(v[i][e], v[i][e], q);
     }
   }
-  return both(q);
+  sum = both(d);
+  squares = both(q);
 }
-__device__ __forceinline__ float inverse_std(float squares, int W, float eps) {
-  return 1.0f / sqrtf(squares / static_cast<float>(W) + eps);
+// 1 / sqrt(var + eps) of deviations with that mean (shift) and sum of squares. The difference of two close
+// numbers may round below 0; squares beyond the range stay infinite (and a NaN a NaN).
+__device__ __forceinline__ float inverse_std(float squares, float shift, float inv_w, float eps) {
+  float var = squares * inv_w;
+  if (var < INFINITY) var = fmaxf(fmaf(-shift, shift, var), 0.0f);
+  return 1.0f / sqrtf(var + eps);
 }
 
 // Rows on their way into shared memory: SLOTS of them, NT tensors a row, in slots that only the
@@ -204,6 +210,7 @@ layer_norm_kernel(const typename R::T* x, const typename R::T* residual, const f
   __shared__ Sums red;
   extern __shared__ __align__(16) unsigned char ring_smem[];
   const int lane = threadIdx.x % R::G;
+  const float inv_w = 1.0f / static_cast<float>(W);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (TPB / R::G);
   int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / R::G) + threadIdx.x / R::G;
   Ring<R, TPB, RES ? 2 : 1, SLOTS> ring;
@@ -249,7 +256,11 @@ layer_norm_kernel(const typename R::T* x, const typename R::T* residual, const f
       for (int i = 0; i < NV; ++i)
         if (R::in(lane, i, W)) store_pack<T, V>(sum_out + base + R::column(lane, i), v[i]);
     }
-    const F2 r = splat(inverse_std(row_sum<R::G>(center<R>(v, W, lane, red, half), red, half), W, eps));
+    float m[2];   // the deviations' sum and that of their squares
+    center<R>(v, W, lane, red, half, m[0], m[1]);
+    row_sums<R::G>(m, red, half);
+    const float shift = m[0] * inv_w, rf = inverse_std(m[1], shift, inv_w, eps);
+    const F2 r = splat(rf), r0 = splat(-shift * rf);   // z = (dev - shift) r
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (R::in(lane, i, W)) {
@@ -260,7 +271,7 @@ layer_norm_kernel(const typename R::T* x, const typename R::T* residual, const f
         }
 #pragma unroll
         for (int e = 0; e < U; ++e)
-          v[i][e] = fma2(mul2(v[i][e], r), kHold ? wh[kHold ? i : 0][e] : wv[e], kHold ? bh[kHold ? i : 0][e] : bv[e]);
+          v[i][e] = fma2(fma2(v[i][e], r, r0), kHold ? wh[kHold ? i : 0][e] : wv[e], kHold ? bh[kHold ? i : 0][e] : bv[e]);
         store_pack<T, V>(out + base + R::column(lane, i), v[i]);
       }
     }
@@ -318,8 +329,10 @@ layer_norm_backward_kernel(const typename R::T* s, const typename R::T* dout, co
       }
     }
     ring.fetch(n, row + SLOTS * stride, rows);
-    // The squares' sum and the two of g are one reduction: z = dev r, so the sum of g z is r times that of g dev.
-    const float squares = center<R>(v, W, lane, red, half);
+    // One reduction for the deviations' sum, that of their squares, and the two of g: z = (dev - shift) r, so the sum of
+    // g z is r times that of g dev less shift times that of g.
+    float m[4];
+    center<R>(v, W, lane, red, half, m[0], m[1]);
     F2 sg = splat(0.f), sgd = splat(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -334,9 +347,12 @@ layer_norm_backward_kernel(const typename R::T* s, const typename R::T* dout, co
         }
       }
     }
-    const float3 m = row_sum<R::G>(make_float3(squares, both(sg), both(sgd)), red, half);
-    const float r = inverse_std(m.x, W, eps);
-    const F2 mg = splat(-m.y * inv_w), mgz = splat(-m.z * r * inv_w), r2 = splat(r);
+    m[2] = both(sg);
+    m[3] = both(sgd);
+    row_sums<R::G>(m, red, half);
+    const float shift = m[0] * inv_w, r = inverse_std(m[1], shift, inv_w, eps);
+    const F2 mg = splat(-m[2] * inv_w), mgz = splat(-fmaf(-shift, m[2], m[3]) * r * inv_w);
+    const F2 r2 = splat(r), r0 = splat(-shift * r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (R::in(lane, i, W)) {
@@ -347,7 +363,7 @@ layer_norm_backward_kernel(const typename R::T* s, const typename R::T* dout, co
         if (SUM) u[i].unpack(o);
 #pragma unroll
         for (int e = 0; e < U; ++e) {
-          const F2 z = mul2(v[i][e], r2);
+          const F2 z = fma2(v[i][e], r2, r0);
           dw[i][e] = fma2(d[i][e], z, dw[i][e]);
           db[i][e] = add2(db[i][e], d[i][e]);
           const F2 g = fma2(d[i][e], kHold ? wh[kHold ? i : 0][e] : wv[e], mg);
