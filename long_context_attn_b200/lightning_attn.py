@@ -426,6 +426,14 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _beyond(name):
+    """The library counts rows, sequences and channels in 32 bits, and ctypes would cut a larger number off."""
+    return LightningAttnError(LA_ERR_UNSUPPORTED, name)
+
+
 def _check_like(ref, *ts):
     """Tensors of ref's shape and dtype, contiguous, all on the current CUDA device."""
     if not ref.is_cuda:
@@ -479,6 +487,8 @@ def new_recurrence_checkpoints(tokens: int, W: int, device="cuda") -> torch.Tens
 
 def lightning_attn_gated_recurrence_workspace_size(num_seqs: int, total_tokens: int, W: int, dtype: int,
                                                    backward: bool = False) -> int:
+    if max(num_seqs, total_tokens, W) > _INT_MAX:
+        return 0
     return int(_lib.lightning_attn_gated_recurrence_workspace_size(num_seqs, total_tokens, W, dtype, int(backward)))
 
 
@@ -491,6 +501,8 @@ def lightning_attn_gated_recurrence(x, f, out, state_in=None, state_out=None, ch
     _check_f32(dev, (B, W), state_in, state_out)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
+    if B > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_gated_recurrence")
     st = _lib.lightning_attn_gated_recurrence(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
                                               _addr(checkpoints), B, T, W, _dtype(x), input_mode, _addr(workspace), n,
                                               _raw_stream(stream, dev))
@@ -507,6 +519,8 @@ def lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, state_in=None,
     _check_f32(dev, (n, W), state_in, state_out)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
+    if total > _INT_MAX or n > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_gated_recurrence_varlen")
     st = _lib.lightning_attn_gated_recurrence_varlen(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
                                                      _addr(checkpoints), _addr(cu_seqlens), n, total, W, _dtype(x),
                                                      input_mode, _addr(workspace), nb, _raw_stream(stream, dev))
@@ -519,6 +533,8 @@ def lightning_attn_gated_recurrence_step(x, f, out, state, input_mode=LA_INPUT_T
     B, W = x.shape
     dev = _check_like(x, f, out)
     _check_f32(dev, (B, W), state)
+    if B > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_gated_recurrence_step")
     st = _lib.lightning_attn_gated_recurrence_step(_addr(x), _addr(f), _addr(out), _addr(state), B, W, _dtype(x),
                                                    input_mode, _raw_stream(stream, dev))
     if st != LA_OK:
@@ -534,6 +550,8 @@ def lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, state_in=None, 
     _check_f32(dev, (B, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
+    if B > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_gated_recurrence_backward")
     st = _lib.lightning_attn_gated_recurrence_backward(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
                                                        _addr(state_in), _addr(dstate_out), _addr(dstate_in),
                                                        _addr(checkpoints), B, T, W, _dtype(x), input_mode,
@@ -553,6 +571,8 @@ def lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu_seqle
     _check_f32(dev, (n, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
+    if total > _INT_MAX or n > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_gated_recurrence_backward_varlen")
     st = _lib.lightning_attn_gated_recurrence_backward_varlen(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
                                                               _addr(state_in), _addr(dstate_out), _addr(dstate_in),
                                                               _addr(checkpoints), _addr(cu_seqlens), n, total, W,
@@ -563,6 +583,8 @@ def lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu_seqle
 
 
 def lightning_attn_layer_norm_workspace_size(rows: int, W: int) -> int:
+    if max(rows, W) > _INT_MAX:
+        return 0
     return int(_lib.lightning_attn_layer_norm_workspace_size(rows, W))
 
 
@@ -572,8 +594,11 @@ def lightning_attn_layer_norm(x, out, residual=None, sum_out=None, weight=None, 
     W = x.shape[-1]
     dev = _check_like(x, out, residual, sum_out)
     _check_f32(dev, (W,), weight, bias)
+    rows = x.numel() // W if W else 0
+    if rows > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_layer_norm")
     st = _lib.lightning_attn_layer_norm(_addr(x), _addr(residual), _addr(weight), _addr(bias), _addr(out), _addr(sum_out),
-                                        x.numel() // W if W else 0, W, _dtype(x), eps, _raw_stream(stream, dev))
+                                        rows, W, _dtype(x), eps, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_layer_norm")
 
@@ -586,9 +611,12 @@ def lightning_attn_layer_norm_backward(s, dout, dx, dsum=None, weight=None, dwei
     dev = _check_like(s, dout, dx, dsum)
     _check_f32(dev, (W,), weight, dweight, dbias)
     n = _check_ws(dev, workspace)
+    rows = s.numel() // W if W else 0
+    if rows > _INT_MAX or W > _INT_MAX:
+        raise _beyond("lightning_attn_layer_norm_backward")
     st = _lib.lightning_attn_layer_norm_backward(_addr(s), _addr(dout), _addr(dsum), _addr(weight), _addr(dx),
-                                                 _addr(dweight), _addr(dbias), s.numel() // W if W else 0, W, _dtype(s),
-                                                 eps, _addr(workspace), n, _raw_stream(stream, dev))
+                                                 _addr(dweight), _addr(dbias), rows, W, _dtype(s), eps,
+                                                 _addr(workspace), n, _raw_stream(stream, dev))
     if st != LA_OK:
         raise LightningAttnError(st, "lightning_attn_layer_norm_backward")
 

@@ -299,6 +299,47 @@ def test_binding_refuses_host_tensors(lib):
         la.lightning_attn_layer_norm_backward(t, t, t.clone())
 
 
+def test_binding_refuses_counts_beyond_32_bits(lib, monkeypatch):
+    """2^32 + 5 rows would reach the library as 5."""
+    import types
+
+    from long_context_attn_b200 import lightning_attn as la
+
+    class Library:
+        calls, lightning_attn_status_string = [], la._lib.lightning_attn_status_string
+
+        def __getattr__(self, name):
+            return lambda *a: self.calls.append(name) or 0
+
+    monkeypatch.setattr(la, "_check_like", lambda *a: 0)
+    monkeypatch.setattr(la, "_check_cu", lambda dev, cu: cu.shape[0] - 1)
+    monkeypatch.setattr(la, "_check_f32", lambda *a: None)
+    st = types.SimpleNamespace(cuda_stream=0)
+    t = lambda *shape: torch.empty(shape, device="meta")  # noqa: E731
+    many = 2 ** 32 + 5
+    calls = {
+        "layer_norm": lambda n: la.lightning_attn_layer_norm(t(n, 2), t(n, 2), stream=st),
+        "layer_norm_backward": lambda n: la.lightning_attn_layer_norm_backward(t(n, 2), t(n, 2), t(n, 2), stream=st),
+        "gated_recurrence": lambda n: la.lightning_attn_gated_recurrence(*[t(1, n, 1)] * 3, stream=st),
+        "gated_recurrence_backward": lambda n: la.lightning_attn_gated_recurrence_backward(*[t(n, 1, 1)] * 5, stream=st),
+        "gated_recurrence_varlen": lambda n: la.lightning_attn_gated_recurrence_varlen(*[t(n, 1)] * 3, t(2), stream=st),
+        "gated_recurrence_backward_varlen":
+            lambda n: la.lightning_attn_gated_recurrence_backward_varlen(*[t(3, 1)] * 5, t(n), stream=st),
+        "gated_recurrence_step": lambda n: la.lightning_attn_gated_recurrence_step(*[t(n, 1)] * 4, stream=st),
+    }
+    for name, call in calls.items():
+        monkeypatch.setattr(la, "_lib", Library())
+        call(7)
+        with pytest.raises(la.LightningAttnError) as err:
+            call(many)
+        assert err.value.status == la.LA_ERR_UNSUPPORTED and name in str(err.value), name
+    assert la._lib.calls == ["lightning_attn_" + name for name in calls]
+    monkeypatch.undo()
+    assert la.lightning_attn_layer_norm_workspace_size(many, 64) == 0
+    assert la.lightning_attn_gated_recurrence_workspace_size(many, 10, 8, 1) == 0
+    assert la.lightning_attn_gated_recurrence_workspace_size(1, many, 8, 1, True) == 0
+
+
 class _Recorder:
     """Stands in for the binding: runs the fp64 references on CPU tensors."""
     from long_context_attn_b200 import lightning_attn as _la
