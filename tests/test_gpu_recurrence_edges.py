@@ -77,3 +77,129 @@ def test_states_that_meet(T, by, cuda_device):
             got.append((a, b, to.clone()))
         la.lightning_attn_check(ws)
         assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def _columns(W):
+    """Some of W channels: the first ones, the last ones and some at the borders of blocks of 16 and 32."""
+    return np.unique(np.r_[0:min(W, 20), max(0, W - 35):W, [c for c in (31, 32, 47, 48, W // 2) if c < W]])
+
+
+def _walk_and_compare(la, x, f, d, s0, ds1, lens, tied, dtype, cu=None):
+    """Forward with checkpoints and backward with and without them: every value written, and those of some channels held
+    to the reference.  x, f, d: packed rows of `lens`, which rows behind them may follow."""
+    import torch
+    W, n, rows, total = x.shape[1], len(lens), sum(lens), x.shape[0]
+    cols = _columns(W)
+    pick = lambda t: None if t is None else _np(t[..., torch.from_numpy(cols).cuda()])  # noqa: E731
+    r = ref.packed(pick(x)[:rows], pick(f)[:rows], lens, tied, pick(s0), pick(d)[:rows], pick(ds1))
+    mode = la.LA_INPUT_TIED if tied else la.LA_INPUT_PLAIN
+    ws, ck = _ws(la, n, total, W, x, True), la.new_recurrence_checkpoints(total, W).fill_(float("nan"))
+    nan = lambda t: torch.full_like(t, float("nan"))  # noqa: E731
+    shape = (n, -1, W) if cu is None else (total, W)
+    view = lambda t: t.view(shape)  # noqa: E731
+    out, s1 = nan(x), torch.full((n, W), float("nan"), device="cuda")
+    if cu is None:
+        la.lightning_attn_gated_recurrence(view(x), view(f), view(out), s0, s1, ck, mode, ws)
+    else:
+        la.lightning_attn_gated_recurrence_varlen(x, f, out, cu, s0, s1, ck, mode, ws)
+    la.lightning_attn_check(ws)
+    assert torch.isfinite(out[:rows]).all() and torch.isfinite(s1).all() and out[rows:].isnan().all()
+    ref.check("out", pick(out)[:rows], r["out"], r["out_tol"], dtype)
+    ref.check("state_out", pick(s1), r["state_out"], r["state_out_tol"])
+    used = -(-rows // 128)
+    assert torch.isfinite(ck[:used]).all()
+    ref.check("checkpoints", pick(ck)[:used], r["enter"][::128], r["enter_tol"][::128])
+    for saved in (ck, None):
+        dx, df, ds0 = nan(x), nan(x), torch.full((n, W), float("nan"), device="cuda")
+        if cu is None:
+            la.lightning_attn_gated_recurrence_backward(view(x), view(f), view(d), view(dx), view(df), s0, ds1, ds0, saved,
+                                                        mode, ws)
+        else:
+            la.lightning_attn_gated_recurrence_backward_varlen(x, f, d, dx, df, cu, s0, ds1, ds0, saved, mode, ws)
+        la.lightning_attn_check(ws)
+        for name, t in (("dx", dx), ("df", df)):
+            assert torch.isfinite(t[:rows]).all() and t[rows:].isnan().all()
+            ref.check(name, pick(t)[:rows], r[name], r[name + "_tol"], dtype)
+        assert torch.isfinite(ds0).all()
+        ref.check("dstate_in", pick(ds0), r["dstate_in"], r["dstate_in_tol"])
+
+
+def _inputs(seed, total, n, W, dtype):
+    """Drawn on the GPU: x, d normal, gates whose channels remember from 2 to about 1000 tokens, states."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    normal = lambda *shape: torch.randn(shape, device="cuda", generator=gen)  # noqa: E731
+    f = normal(total, W) + 7 * torch.rand(W, device="cuda", generator=gen)
+    return normal(total, W).to(t), f.to(t), normal(total, W).to(t), normal(n, W), normal(n, W)
+
+
+# Lone CTAs (more than 98 blocks of 32 channels), over 5 tiles and more: whole vectors, odd rows, several sequences.
+WIDE = [(1, 1500, 3200), (2, 900, 4096), (1, 1333, 3205), (3, 700, 4104), (1, 1290, 8192), (1, 129, 3300)]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("B,T,W", WIDE)
+def test_wide_fixed(B, T, W, tied, dtype, cuda_device):
+    torch, la = _torch()
+    x, f, d, s0, ds1 = _inputs(B + T + W, B * T, B, W, dtype)
+    _walk_and_compare(la, x, f, d, s0, ds1, [T] * B, tied, dtype)
+
+
+# Clusters of every size that the width gives, over several rounds: 3 to 8 CTAs (blocks of 16 channels in the fp32 forward,
+# of 32 otherwise), a last round that is not full.
+CLUSTERS = [(1, 6100, 600), (1, 6100, 800), (1, 5000, 1001), (1, 6100, 1104), (2, 3333, 1300), (1, 6100, 1504), (1, 6100, 1600),
+            (1, 6100, 2000), (3, 2000, 2303), (1, 6100, 2400), (1, 4500, 3136)]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("B,T,W", CLUSTERS)
+def test_clusters_of_every_size(B, T, W, dtype, cuda_device):
+    torch, la = _torch()
+    x, f, d, s0, ds1 = _inputs(B + T + W, B * T, B, W, dtype)
+    _walk_and_compare(la, x, f, d, s0, ds1, [T] * B, W % 16 == 0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tied,W", [(True, 3200), (False, 3205), (False, 4096), (True, 2000), (False, 1300), (True, 1001)])
+@pytest.mark.parametrize("lens", [[700, 0, 1, 333, 260, 128, 2, 0, 515], [1, 1900, 40], [5] * 300])
+def test_wide_and_clusters_packed(lens, tied, W, dtype, cuda_device):
+    torch, la = _torch()
+    rows = sum(lens)
+    x, f, d, s0, ds1 = _inputs(rows + W, rows + 90, len(lens), W, dtype)
+    for t in (x, f, d):
+        t[rows:] = float("nan")
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+    _walk_and_compare(la, x, f, d, s0, ds1, lens, tied, dtype, cu)
+
+
+def test_values_beyond_32_bit_offsets(cuda_device):
+    """More than 2^31 values a tensor, all of them drawn: a sequence of 262300 tokens, its first and last channels held to
+    the reference from the first row to the last."""
+    torch, la = _torch()
+    W, lens = 8192, [262300, 150]
+    total = sum(lens)
+    assert lens[0] * W > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    draw = lambda: torch.empty(total, W, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)  # noqa: E731
+    x, d = draw(), draw()
+    f = draw().add_(3.0)
+    out = torch.full_like(x, float("nan"))
+    s1, ds0 = (torch.full((2, W), float("nan"), device="cuda") for _ in range(2))
+    ck, ws = la.new_recurrence_checkpoints(total, W), _ws(la, 2, total, W, x, True)
+    cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+    cols = np.r_[0:3, 4100, W - 3:W]
+    pick = lambda t: _np(t[:, torch.from_numpy(cols).cuda()])  # noqa: E731
+    r = ref.packed(pick(x), pick(f), lens, True, None, pick(d))
+    la.lightning_attn_gated_recurrence_varlen(x, f, out, cu, None, s1, ck, workspace=ws)
+    ref.check("out", pick(out), r["out"], r["out_tol"], "bf16")
+    ref.check("state_out", pick(s1), r["state_out"], r["state_out_tol"])
+    ref.check("checkpoints", pick(ck), r["enter"][::128], r["enter_tol"][::128])
+    dx, df = out.fill_(float("nan")), torch.full_like(x, float("nan"))
+    la.lightning_attn_gated_recurrence_backward_varlen(x, f, d, dx, df, cu, None, None, ds0, ck, workspace=ws)
+    la.lightning_attn_check(ws)
+    ref.check("dx", pick(dx), r["dx"], r["dx_tol"], "bf16")
+    ref.check("df", pick(df), r["df"], r["df_tol"], "bf16")
+    ref.check("dstate_in", pick(ds0), r["dstate_in"], r["dstate_in_tol"])
+    assert all(torch.isfinite(t[i:i + 65536]).all() for t in (dx, df) for i in range(0, total, 65536))
