@@ -860,25 +860,29 @@ cudaError_t launch_kernel(K kernel, int nblocks, int cluster, size_t smem, const
   c.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&c, kernel, p);
 }
-// CTAs that walk a block of channels together, `blocks` of them fitting an SM.  A tile takes an SM
-// 1.5 us with one CTA on it and 1.3 us with two; a round of a cluster takes 2.5 to 2.9 us with one CTA an
-// SM, 3.9 us with two (bf16, 8192 values a tile, measured at 131072 x 1024: 788 us alone, 636, 367, 252
-// us in clusters of 2, 4, 8).  So clusters of three or more, and none where two would fit: 32768 x 4096
-// takes 205 us with 128 CTAs alone and 223 us in pairs.  A cluster lies in one group of SMs: 16 where
-// there are few enough of them; sizes of 9 to 15 left part of the GPU idle (131072 x 1024: 374 us with 9).
+// CTAs that walk a block of channels together, `blocks` of them fitting an SM: as many as there is room for, from three up
+// (bf16, 131072 x 1024: 834 us alone, 512, 349, 269, 240 in clusters of 2, 3, 4, 8; in pairs where two would fit,
+// 32768 x 4096 takes 202 us, 215 alone).  9 to 15 left part of the GPU idle (131072 x 1024: 374 us with 9), so it is 8 or 16.
+// Room for all CTAs is not room for all clusters, which lie in one group of SMs each: 14 of 16 CTAs run at once in bf16, and 15
+// blocks wait for one another (65536 x 480: 102 us, 76 in clusters of 8; 16 to 18 blocks: 102 against 110); likewise 94 to 98 blocks in
+// threes (32768 x 3008: 214 us, 213 alone).
 int cluster_for(int nblocks, int64_t tiles, int blocks, int most) {
-  int fit = nblocks <= 14 ? 16 : blocks * sm_count() / nblocks;
+  int fit = blocks * sm_count() / nblocks;
   if (fit > most) fit = most;
   int n = fit >= 16 ? 16 : fit > 8 ? 8 : fit;
   if (n > tiles) n = static_cast<int>(tiles);
   if (n > 8 && n < 16) n = 8;
   return n < 3 ? 1 : n;
 }
-template <class S, bool TIED, int BLOCKS> cudaError_t launch_forward(RecArgs p, cudaStream_t stream) {
+// CLUSTERS: where there are few channels; false for a shape that is only taken where there are many.
+template <class S, bool TIED, int BLOCKS, bool CLUSTERS> cudaError_t launch_forward(RecArgs p, cudaStream_t stream) {
   p.nblocks = (p.W + S::C - 1) / S::C;
-  const int cluster = cluster_for(p.nblocks, (p.tokens + S::L - 1) / S::L, BLOCKS, kMaxCluster);
-  return cluster > 1 ? launch_kernel(rec_forward_kernel<S, TIED, true, BLOCKS>, p.nblocks, cluster, sizeof(ForwardSmem<S, true>), p, stream)
-                     : launch_kernel(rec_forward_kernel<S, TIED, false, BLOCKS>, p.nblocks, 1, sizeof(ForwardSmem<S, false>), p, stream);
+  if constexpr (CLUSTERS) {
+    const int cluster = cluster_for(p.nblocks, (p.tokens + S::L - 1) / S::L, BLOCKS, kMaxCluster);
+    if (cluster > 1)
+      return launch_kernel(rec_forward_kernel<S, TIED, true, BLOCKS>, p.nblocks, cluster, sizeof(ForwardSmem<S, true>), p, stream);
+  }
+  return launch_kernel(rec_forward_kernel<S, TIED, false, BLOCKS>, p.nblocks, 1, sizeof(ForwardSmem<S, false>), p, stream);
 }
 template <class S, bool TIED> cudaError_t launch_backward(RecArgs p, cudaStream_t stream) {
   p.nblocks = (p.W + S::C - 1) / S::C;
@@ -888,17 +892,20 @@ template <class S, bool TIED> cudaError_t launch_backward(RecArgs p, cudaStream_
                      : launch_kernel(rec_backward_kernel<S, TIED, false>, p.nblocks, 1, sizeof(BackwardSmem<S, false>), p, stream);
 }
 // bf16: tiles of 256 rows x 32 channels, 16 rows a thread; fp32, whose rows are twice the bytes: 128 x 32, 8
-// rows a thread.  The fp32 forward in clusters takes 256 x 16, so that three CTAs fit an SM and there are
-// more blocks to share (65536 x 768: 154 us against 204; the backward, 319 against 262, does not).
+// rows a thread.  The fp32 forward takes 256 x 16 where blocks of 32 would be so few that three CTAs or more share one
+// (up to 98 blocks on 148 SMs), whatever the length: three of its CTAs fit an SM and there are more blocks to share (65536 x 768:
+// 140 us against 204; the backward, 319 against 262, does not), and 256 rows are one tile, not two (2048 channels: 200 rows 3.9 us
+// against 5.8, 400 rows 6.1 against 6.8, 4000 rows 31 against 27).  Above 148 blocks of 16 it walks without clusters, where clusters of
+// three with blocks of 32 would be faster from 4000 rows on (32768 x 2400: 284 us against 206).
 template <typename T, bool VEC, bool TIED> cudaError_t launch_typed(const RecArgs& p, bool backward, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
     using S = Shape<T, 16, 16, VEC>;
-    return backward ? launch_backward<S, TIED>(p, stream) : launch_forward<S, TIED, 2>(p, stream);
+    return backward ? launch_backward<S, TIED>(p, stream) : launch_forward<S, TIED, 2, true>(p, stream);
   } else {
     using S = Shape<T, 16, 8, VEC>;
     if (backward) return launch_backward<S, TIED>(p, stream);
-    if (cluster_for((p.W + 31) / 32, p.tokens, 2, kMaxCluster) > 1) return launch_forward<Shape<T, 8, 8, VEC>, TIED, 3>(p, stream);
-    return launch_forward<S, TIED, 2>(p, stream);
+    if ((p.W + S::C - 1) / S::C * 3 <= 2 * sm_count()) return launch_forward<Shape<T, 8, 8, VEC>, TIED, 3, true>(p, stream);
+    return launch_forward<S, TIED, 2, false>(p, stream);
   }
 }
 template <typename T> cudaError_t launch_walk(const RecArgs& p, bool vec, bool backward, cudaStream_t stream) {
