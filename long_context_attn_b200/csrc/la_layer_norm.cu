@@ -429,8 +429,6 @@ __global__ void __launch_bounds__(1024) layer_norm_weight_sum_kernel(const float
   }
 }
 
-constexpr int kMaxParts = 1184;   // CTAs of the backward pass: at most 8 for each of 148 SMs
-
 struct LnArgs {
   const void *x, *residual, *dout, *dsum;
   const float *w, *b;
@@ -448,10 +446,8 @@ int sm_count() {
   return n;
 }
 // CTAs: one for each TPB / G rows, no more than fit at once.
-unsigned ln_grid(int rows, int per, int blocks, int most) {
-  const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
-  int64_t fit = static_cast<int64_t>(blocks) * sm_count();
-  if (fit > most) fit = most;
+unsigned ln_grid(int rows, int per, int blocks) {
+  const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per, fit = static_cast<int64_t>(blocks) * sm_count();
   return static_cast<unsigned>(need < fit ? need : fit);
 }
 constexpr int clamp_slots(int n) { return n < 1 ? 1 : n > 4 ? 4 : n; }
@@ -472,18 +468,24 @@ template <class R, bool RES> cudaError_t ln_forward(const LnArgs& a) {
     if (e != cudaSuccess) return e;
   }
   const int per = TPB / G;
-  const unsigned grid = kStay ? ln_grid(a.rows, per, BLOCKS, INT32_MAX) : static_cast<unsigned>((a.rows - 1) / per + 1);
+  const unsigned grid = kStay ? ln_grid(a.rows, per, BLOCKS) : static_cast<unsigned>((a.rows - 1) / per + 1);
   kernel<<<grid, TPB, smem, a.stream>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.w, a.b,
                                         static_cast<T*>(a.out), static_cast<T*>(a.sum_out), a.rows, a.W, a.eps);
   return cudaGetLastError();
 }
+// The backward's CTAs: as many threads an SM as the sums' registers allow, in no more than 8 CTAs. Each has a part of the
+// sums to write and to be added, and more of them cost more than their threads gain: of 64 threads, 8 against 10
+// (fp32) or 16: 65536 x 600 fp32 115 us against 122, 131072 x 512 bf16 94 against 101, 3000 x 512 17 against 25 (only rows read
+// element by element gain: 100000 x 129 107 against 77).
+template <int V, int NV, int G> struct Back {
+  static constexpr int TPB = G == 32 ? 256 : G, per = TPB / G;
+  static constexpr int THREADS = NV * V <= 8 ? 1024 : 512;   // NV * V values of a row, and of each sum, in a thread
+  static constexpr int FIT = THREADS / TPB, BLOCKS = FIT < 1 ? 1 : FIT > 8 ? 8 : FIT;
+};
 template <class R, bool SUM> cudaError_t ln_backward(const LnArgs& a) {
   using T = typename R::T;
-  constexpr int G = R::G, TPB = G == 32 ? 256 : G, per = TPB / G;
-  constexpr int kValues = R::NV * R::V;   // of a row, and of each sum, in a thread
-  // threads an SM: as many as their sums' registers allow (65537 x 768 fp32: 117 us with 640, 141 with 512)
-  constexpr int THREADS = kValues <= 8 ? 1024 : kValues <= 12 ? 640 : 512;   // an SM, by the registers of the sums
-  constexpr int BLOCKS = THREADS / TPB > 0 ? THREADS / TPB : 1;
+  using S = Back<R::V, R::NV, R::G>;
+  constexpr int TPB = S::TPB, per = S::per, BLOCKS = S::BLOCKS;
   constexpr int SLOTS = R::V == 1 ? 0 : clamp_slots(200 * 1024 / (BLOCKS * TPB) / 16 / ((SUM ? 3 : 2) * R::NV));
   constexpr size_t ring = Ring<R, TPB, SUM ? 3 : 2, SLOTS>::kBytes;
   const size_t fold = per == 1 ? 0 : 2 * sizeof(float) * a.W, smem = ring > fold ? ring : fold;
@@ -492,7 +494,7 @@ template <class R, bool SUM> cudaError_t ln_backward(const LnArgs& a) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const unsigned grid = ln_grid(a.rows, per, BLOCKS, kMaxParts);
+  const unsigned grid = ln_grid(a.rows, per, BLOCKS);
   kernel<<<grid, TPB, smem, a.stream>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.dout),
                                         static_cast<const T*>(a.dsum), a.w, static_cast<T*>(a.out), a.partial, a.rows,
                                         a.W, a.eps);
@@ -515,36 +517,51 @@ template <typename T, int V, int NV, int G> cudaError_t ln_bwd(const LnArgs& a) 
     return a.dsum ? ln_backward<Row<T, V, NV, G, V != 1>, true>(a) : ln_backward<Row<T, V, NV, G, V != 1>, false>(a);
   return a.dsum ? ln_backward<Row<T, V, NV, G, false>, true>(a) : ln_backward<Row<T, V, NV, G, false>, false>(a);
 }
+template <int NV_, int G_> struct Band {
+  static constexpr int NV = NV_, G = G_;
+};
+template <int V, class F> auto forward_band(int W, F f) {
+  const int vecs = (W + V - 1) / V;
+  if (vecs <= 32) return f(Band<1, 32>{});
+  if (vecs <= 64) return f(Band<2, 32>{});
+  if (vecs <= 128) return f(Band<4, 32>{});
+  if (vecs <= 192) return f(Band<3, 64>{});
+  if (vecs <= 256) return f(Band<2, 128>{});
+  if (vecs <= 512) return f(Band<2, 256>{});
+  if (vecs <= 1024) return f(Band<2, 512>{});
+  if constexpr (V == 8) return f(Band<4, 512>{});
+  if (vecs <= 2048) return f(Band<4, 512>{});
+  if constexpr (V == 4) return f(Band<4, 1024>{});
+  if (vecs <= 4096) return f(Band<4, 1024>{});
+  return f(Band<16, 1024>{});
+}
+template <int V, class F> auto backward_band(int W, F f) {
+  const int vecs = (W + V - 1) / V;
+  if (vecs <= 32) return f(Band<1, 32>{});
+  if (vecs <= 64) return f(Band<1, 64>{});
+  if (vecs <= 128) return f(Band<1, 128>{});
+  if (vecs <= 192) return f(Band<3, 64>{});
+  if (vecs <= 256) return f(Band<2, 128>{});
+  if (vecs <= 512) return f(Band<2, 256>{});
+  if (vecs <= 1024) return f(Band<2, 512>{});
+  if constexpr (V == 8) return f(Band<4, 512>{});
+  if (vecs <= 2048) return f(Band<4, 512>{});
+  if constexpr (V == 4) return f(Band<4, 1024>{});
+  if (vecs <= 4096) return f(Band<4, 1024>{});
+  return f(Band<16, 1024>{});
+}
+static_assert(kMaxNormWidth <= 16384, "the widest band");
 template <typename T, int V> cudaError_t ln_launch(const LnArgs& a, bool backward) {
-  const int vecs = (a.W + V - 1) / V;
-  if (!backward) {
-    if (vecs <= 32) return ln_fwd<T, V, 1, 32>(a);
-    if (vecs <= 64) return ln_fwd<T, V, 2, 32>(a);
-    if (vecs <= 128) return ln_fwd<T, V, 4, 32>(a);
-    if (vecs <= 192) return ln_fwd<T, V, 3, 64>(a);
-    if (vecs <= 256) return ln_fwd<T, V, 2, 128>(a);
-    if (vecs <= 512) return ln_fwd<T, V, 2, 256>(a);
-    if (vecs <= 1024) return ln_fwd<T, V, 2, 512>(a);
-    if (vecs <= 2048) return ln_fwd<T, V, 4, 512>(a);
-    if constexpr (V < 8) {
-      if (vecs <= 4096) return ln_fwd<T, V, 4, 1024>(a);
-    }
-    if constexpr (V == 1) return ln_fwd<T, V, 16, 1024>(a);
-  } else {
-    if (vecs <= 32) return ln_bwd<T, V, 1, 32>(a);
-    if (vecs <= 64) return ln_bwd<T, V, 1, 64>(a);
-    if (vecs <= 128) return ln_bwd<T, V, 1, 128>(a);
-    if (vecs <= 192) return ln_bwd<T, V, 3, 64>(a);
-    if (vecs <= 256) return ln_bwd<T, V, 2, 128>(a);
-    if (vecs <= 512) return ln_bwd<T, V, 2, 256>(a);
-    if (vecs <= 1024) return ln_bwd<T, V, 2, 512>(a);
-    if (vecs <= 2048) return ln_bwd<T, V, 4, 512>(a);
-    if constexpr (V < 8) {
-      if (vecs <= 4096) return ln_bwd<T, V, 4, 1024>(a);
-    }
-    if constexpr (V == 1) return ln_bwd<T, V, 16, 1024>(a);
-  }
-  return cudaErrorInvalidValue;
+  if (backward)
+    return backward_band<V>(a.W, [&](auto b) { return ln_bwd<T, V, decltype(b)::NV, decltype(b)::G>(a); });
+  return forward_band<V>(a.W, [&](auto b) { return ln_fwd<T, V, decltype(b)::NV, decltype(b)::G>(a); });
+}
+// How many parts of the sums the backward's CTAs write: what its grid is, and its workspace.
+template <int V> size_t ln_parts(int rows, int W) {
+  return backward_band<V>(W, [&](auto b) -> size_t {
+    using S = Back<V, decltype(b)::NV, decltype(b)::G>;
+    return ln_grid(rows, S::per, S::BLOCKS);
+  });
 }
 
 cudaError_t launch_layer_norm(const LnArgs& a, la_dtype dt, bool backward) {
@@ -554,9 +571,11 @@ cudaError_t launch_layer_norm(const LnArgs& a, la_dtype dt, bool backward) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Of either type.
 size_t ln_ws_bytes(int rows, int W) {
-  const size_t parts = static_cast<size_t>(rows < kMaxParts ? rows : kMaxParts);
-  const size_t n = sizeof(float) * 2 * W * parts;
+  const size_t bf16 = W % 8 == 0 ? ln_parts<8>(rows, W) : ln_parts<1>(rows, W);
+  const size_t f32 = W % 4 == 0 ? ln_parts<4>(rows, W) : ln_parts<1>(rows, W);
+  const size_t n = sizeof(float) * 2 * W * (bf16 > f32 ? bf16 : f32);
   return n < 256 ? 256 : (n + 255) & ~size_t(255);
 }
 

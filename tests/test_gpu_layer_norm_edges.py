@@ -85,3 +85,25 @@ def test_rows_far_from_zero(mean, W, cuda_device):
     z = dev * r
     tol = dev_tol * r + np.abs(z) * (0.5 * var_tol * r * r + 8 * U) + 2 * U * (delta * r + np.abs(z))
     ref.check("out", _np(out), z, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 150, 5000])
+@pytest.mark.parametrize("W", [7, 40, 128, 200, 256, 260, 500, 512, 768, 1000, 1024, 1500, 2048, 4000, 8192, 8190, 16384])
+def test_workspace_of_the_size_asked_for(W, rows, dtype, cuda_device):
+    """What lies behind the workspace stays as it was, and the sums are those of a larger one."""
+    torch, la = _torch()
+    s, d = (torch.randn(rows, W, device="cuda").to(_dtype(dtype)) for _ in range(2))
+    size = la.lightning_attn_layer_norm_workspace_size(rows, W)
+    got = []
+    for room in (size, size + 4096):
+        buf = torch.full((size + 8192,), 0xAB, dtype=torch.uint8, device="cuda")
+        dx, dw, db = torch.empty_like(s), torch.empty(W, device="cuda"), torch.empty(W, device="cuda")
+        la.lightning_attn_layer_norm_backward(s, d, dx, dweight=dw, dbias=db, eps=EPS, workspace=buf[:room])
+        assert (buf[size:] == 0xAB).all()
+        got.append((dx, dw, db))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    with pytest.raises(la.LightningAttnError):
+        la.lightning_attn_layer_norm_backward(s, d, dx, dweight=dw, eps=EPS, workspace=buf[:size - 1])
+    n = (rows + 16) * U
+    ref.check("dbias", _np(got[0][2]), _np(d).sum(0), n * np.abs(_np(d)).sum(0))

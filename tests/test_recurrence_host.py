@@ -283,6 +283,19 @@ def test_layer_norm_entries_refuse_overlaps(lib):
         assert g(**kw) == 3, kw
 
 
+def test_layer_norm_workspace_is_what_the_launch_uses(lib):
+    """A part of the sums, 2 W floats, for each CTA that the rows make or that fits: at most 8 on each of 148 SMs, one of
+    them for wide rows."""
+    if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the numbers are for 148 SMs")
+    size = lib.lightning_attn_layer_norm_workspace_size
+    size.restype = ctypes.c_size_t
+    up = lambda n: (n + 255) & ~255  # noqa: E731
+    for rows, W, parts in ((8192, 8192, 148), (100000, 16384, 148), (256, 8192, 148), (100, 8192, 100), (100000, 512, 1184),
+                           (100000, 128, 592), (64, 128, 8), (1, 16384, 1)):
+        assert size(rows, W) == up(parts * 2 * W * 4), (rows, W, size(rows, W) // (8 * W))
+
+
 # --------------------------------------------------------------------------- binding
 def test_binding_refuses_host_tensors(lib):
     from long_context_attn_b200 import lightning_attn as la
