@@ -111,7 +111,10 @@ __device__ __forceinline__ float both(F2 a) {
   return v.x + v.y;
 }
 
-// How a row lies in its G threads: NV vectors of V values each; FULL: exactly.
+// How a row lies in its G threads: NV vectors of V values each; FULL: exactly, so that no column is asked whether it is
+// inside. It costs a second kernel of each vector form and gains on the widths that models mostly have
+// (bf16, residual, forward and backward: 65536 x 1024 93 and 107 us against 121 and 120, 16384 x 4096 100 and 105 against 101 and
+// 113, 8192 x 8192 99 and 112 against 97 and 125).
 template <typename T_, int V_, int NV_, int G_, bool FULL_> struct Row {
   using T = T_;
   static constexpr int V = V_, NV = NV_, G = G_, U = pairs(V_);
@@ -506,7 +509,10 @@ template <class R, bool SUM> cudaError_t ln_backward(const LnArgs& a) {
 
 // The threads that share a row and how much of it each holds, by the row's vectors.  The backward's sums
 // take registers, so its rows have more threads with less each (8192 wide: 512 threads of two vectors 117
-// us, 1024 of one 144; 65536 x 1024: 128 threads of one vector 114 us, a warp of four 215).
+// us, 1024 of one 144; 65536 x 1024: 128 threads of one vector 114 us, a warp of four 215).  Rows of 129 to 192 vectors lie
+// in 64 threads of three, not in 128 of two: fp32 65536 x 520 61 us against 91, its backward 81 against 116, 65537 x 768 70
+// against 95 and 114 against 124, bf16 32768 x 1280 48 against 66; but the bf16 backward in 128 (32768 x 1280: 76
+// us against 92, 32768 x 1536 82 against 92).
 template <typename T, int V, int NV, int G> cudaError_t ln_fwd(const LnArgs& a) {
   if (V > 1 && a.W == V * NV * G)
     return a.residual ? ln_forward<Row<T, V, NV, G, V != 1>, true>(a) : ln_forward<Row<T, V, NV, G, V != 1>, false>(a);
@@ -540,7 +546,7 @@ template <int V, class F> auto backward_band(int W, F f) {
   if (vecs <= 32) return f(Band<1, 32>{});
   if (vecs <= 64) return f(Band<1, 64>{});
   if (vecs <= 128) return f(Band<1, 128>{});
-  if (vecs <= 192) return f(Band<3, 64>{});
+  if (vecs <= 192 && V < 8) return f(Band<3, 64>{});   // of 8 values they and both their sums are 72 registers
   if (vecs <= 256) return f(Band<2, 128>{});
   if (vecs <= 512) return f(Band<2, 256>{});
   if (vecs <= 1024) return f(Band<2, 512>{});
