@@ -934,14 +934,15 @@ cudaError_t launch_rec(RecArgs p, la_dtype dt, bool backward, void* workspace,
   const float*& from = backward ? p.ds1 : p.s0;
   float* to = backward ? p.ds0 : p.s1;
   const size_t bytes = sizeof(float) * static_cast<size_t>(p.nseq) * p.W;
-  if (p.tokens == 0 && (!to || from == to)) return cudaSuccess;
+  const bool pass = p.tokens == 0 && !p.cu;   // no rows: the states pass through (packed: in the kernel, which checks the offsets)
+  if (pass && (!to || from == to)) return cudaSuccess;
   if (overlap(from, bytes, to, bytes)) {
     float* copy = reinterpret_cast<float*>(base);
     const cudaError_t e = cudaMemcpyAsync(copy, from, bytes, cudaMemcpyDeviceToDevice, stream);
     if (e != cudaSuccess) return e;
     from = copy;
   }
-  if (p.tokens == 0)   // no rows: the states pass through
+  if (pass)
     return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream) : cudaMemsetAsync(to, 0, bytes, stream);
   const bool vec = vectors(p.W, dt);
   return dt == LA_BF16 ? launch_walk<uint16_t>(p, vec, backward, stream) : launch_walk<float>(p, vec, backward, stream);

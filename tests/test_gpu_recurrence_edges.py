@@ -203,3 +203,40 @@ def test_values_beyond_32_bit_offsets(cuda_device):
     ref.check("df", pick(df), r["df"], r["df_tol"], "bf16")
     ref.check("dstate_in", pick(ds0), r["dstate_in"], r["dstate_in_tol"])
     assert all(torch.isfinite(t[i:i + 65536]).all() for t in (dx, df) for i in range(0, total, 65536))
+
+
+@pytest.mark.parametrize("B", [3, 5000])
+def test_malformed_offsets_without_rows(B, cuda_device):
+    """Packed batches of no rows: offsets other than zeros are reported, forward and backward; with zeros the states
+    pass through, into buffers of their own, in place and shifted."""
+    torch, la = _torch()
+    W = 40
+    x = torch.empty(0, W, device="cuda")
+    e = lambda: torch.empty_like(x)  # noqa: E731
+    ws = _ws(la, B, 0, W, x, True)
+    zero = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+
+    def call(backward, cu, given, to):
+        if backward:
+            la.lightning_attn_gated_recurrence_backward_varlen(x, x, x, e(), e(), cu, None, given, to, workspace=ws)
+        else:
+            la.lightning_attn_gated_recurrence_varlen(x, x, e(), cu, given, to, workspace=ws)
+
+    for backward in (False, True):
+        for at, value in ((B, 3), (1, -1), (0, 1), (2, 1)):
+            cu = zero.clone()
+            cu[at] = value
+            call(backward, cu, None, None)
+            with pytest.raises(la.LightningAttnError) as err:
+                la.lightning_attn_check(ws)
+            assert err.value.status == la.LA_ERR_DEVICE
+        s = torch.randn(B, W, device="cuda")
+        for by in (0, 1, None):
+            buf = torch.empty(B + 1, W, device="cuda")
+            first = buf[:B].copy_(s)
+            last = torch.empty_like(s) if by is None else buf[by:by + B]
+            call(backward, zero, first, last)
+            assert torch.equal(last, s)
+        call(backward, zero, None, last)
+        assert not last.any()
+        la.lightning_attn_check(ws)
