@@ -978,10 +978,12 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
       {p.ds1, states, false, kBegin}, {p.ds0, states, true, kEndOfWalk}, {p.ck, cks, !backward, kNever},
       {p.out, rows, true, kNever}, {p.dx, rows, true, kNever}, {p.df, rows, true, kNever},
       {workspace, l.total, true, kNever}};
-  for (const auto& w : args)
+  for (const auto& w : args) {
+    if (!w.written || !w.at) continue;
     for (const auto& t : args)
-      if (w.written && &t != &w && !(w.walk == kEndOfWalk && t.walk == kBegin) && overlap(w.at, w.bytes, t.at, t.bytes))
+      if (t.at && &t != &w && !(w.walk == kEndOfWalk && t.walk == kBegin) && overlap(w.at, w.bytes, t.at, t.bytes))
         return LA_ERR_INVALID_ARG;
+  }
   p.err = static_cast<ErrRec*>(workspace);
   p.tied = mode == LA_INPUT_TIED;
   cudaError_t e = cudaSuccess;

@@ -426,7 +426,7 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-_INT_MAX = 2 ** 31 - 1
+_INT_MAX = 2 ** 31 - 1    # (a | b) is above it where one of them is
 
 
 def _beyond(name):
@@ -501,7 +501,7 @@ def lightning_attn_gated_recurrence(x, f, out, state_in=None, state_out=None, ch
     _check_f32(dev, (B, W), state_in, state_out)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
-    if B > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
+    if (B | T | W) > _INT_MAX:
         raise _beyond("lightning_attn_gated_recurrence")
     st = _lib.lightning_attn_gated_recurrence(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
                                               _addr(checkpoints), B, T, W, _dtype(x), input_mode, _addr(workspace), n,
@@ -519,7 +519,7 @@ def lightning_attn_gated_recurrence_varlen(x, f, out, cu_seqlens, state_in=None,
     _check_f32(dev, (n, W), state_in, state_out)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
-    if total > _INT_MAX or n > _INT_MAX or W > _INT_MAX:
+    if (total | n | W) > _INT_MAX:
         raise _beyond("lightning_attn_gated_recurrence_varlen")
     st = _lib.lightning_attn_gated_recurrence_varlen(_addr(x), _addr(f), _addr(out), _addr(state_in), _addr(state_out),
                                                      _addr(checkpoints), _addr(cu_seqlens), n, total, W, _dtype(x),
@@ -533,7 +533,7 @@ def lightning_attn_gated_recurrence_step(x, f, out, state, input_mode=LA_INPUT_T
     B, W = x.shape
     dev = _check_like(x, f, out)
     _check_f32(dev, (B, W), state)
-    if B > _INT_MAX or W > _INT_MAX:
+    if (B | W) > _INT_MAX:
         raise _beyond("lightning_attn_gated_recurrence_step")
     st = _lib.lightning_attn_gated_recurrence_step(_addr(x), _addr(f), _addr(out), _addr(state), B, W, _dtype(x),
                                                    input_mode, _raw_stream(stream, dev))
@@ -550,7 +550,7 @@ def lightning_attn_gated_recurrence_backward(x, f, dout, dx, df, state_in=None, 
     _check_f32(dev, (B, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-B * T // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     n = _check_ws(dev, workspace)
-    if B > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
+    if (B | T | W) > _INT_MAX:
         raise _beyond("lightning_attn_gated_recurrence_backward")
     st = _lib.lightning_attn_gated_recurrence_backward(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
                                                        _addr(state_in), _addr(dstate_out), _addr(dstate_in),
@@ -571,7 +571,7 @@ def lightning_attn_gated_recurrence_backward_varlen(x, f, dout, dx, df, cu_seqle
     _check_f32(dev, (n, W), state_in, dstate_out, dstate_in)
     _check_f32(dev, (-(-total // LA_RECURRENCE_CHECKPOINT_ROWS), W), checkpoints)
     nb = _check_ws(dev, workspace)
-    if total > _INT_MAX or n > _INT_MAX or W > _INT_MAX:
+    if (total | n | W) > _INT_MAX:
         raise _beyond("lightning_attn_gated_recurrence_backward_varlen")
     st = _lib.lightning_attn_gated_recurrence_backward_varlen(_addr(x), _addr(f), _addr(dout), _addr(dx), _addr(df),
                                                               _addr(state_in), _addr(dstate_out), _addr(dstate_in),
@@ -595,7 +595,7 @@ def lightning_attn_layer_norm(x, out, residual=None, sum_out=None, weight=None, 
     dev = _check_like(x, out, residual, sum_out)
     _check_f32(dev, (W,), weight, bias)
     rows = x.numel() // W if W else 0
-    if rows > _INT_MAX or W > _INT_MAX:
+    if (rows | W) > _INT_MAX:
         raise _beyond("lightning_attn_layer_norm")
     st = _lib.lightning_attn_layer_norm(_addr(x), _addr(residual), _addr(weight), _addr(bias), _addr(out), _addr(sum_out),
                                         rows, W, _dtype(x), eps, _raw_stream(stream, dev))
@@ -612,7 +612,7 @@ def lightning_attn_layer_norm_backward(s, dout, dx, dsum=None, weight=None, dwei
     _check_f32(dev, (W,), weight, dweight, dbias)
     n = _check_ws(dev, workspace)
     rows = s.numel() // W if W else 0
-    if rows > _INT_MAX or W > _INT_MAX:
+    if (rows | W) > _INT_MAX:
         raise _beyond("lightning_attn_layer_norm_backward")
     st = _lib.lightning_attn_layer_norm_backward(_addr(s), _addr(dout), _addr(dsum), _addr(weight), _addr(dx),
                                                  _addr(dweight), _addr(dbias), rows, W, _dtype(s), eps,
