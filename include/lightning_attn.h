@@ -437,7 +437,9 @@ LA_API la_status lightning_attn_chunk_state(const void* k, const void* v, const 
  *   B, T, W      B >= 1, T >= 0 (T == 0: no output; state_out = state_in or zeros), W >= 1
  *                (LA_ERR_UNSUPPORTED: B > 2^28, W > 2^22, B*T > 2^31 - 1).  Rows whose bytes
  *                are a multiple of 16 are read as 16-byte vectors; others element by element
- *                (slower, same results).
+ *                (slower, same results).  A block of 32 channels is one CTA's from 99 blocks up, two
+ *                fitting an SM, so a value costs least just below a multiple of 2 * 148 blocks
+ *                (9472 channels) and most just above one.
  *   workspace    device scratch of >= lightning_attn_gated_recurrence_workspace_size bytes,
  *                256-byte aligned, its first 256 bytes (the error record, as for the
  *                prefill) zero before its first use; the call uses the rest only where

@@ -6,11 +6,13 @@
 //
 // A row stays in the registers of the G threads that share it (a warp, or a CTA) between its
 // one read and its one write, so the deviations are squared after the mean is known and both
-// passes touch memory once: memory is the bound.  What keeps wide rows from it is the latency of a
+// passes touch memory once.  Memory is the forward's bound.  What keeps wide rows from it is the latency of a
 // row's reductions with few rows on an SM, so CTAs stay and have the next rows on their way while
 // they reduce one.  8192 x 8192 bf16 with the residual (537 MB): forward 121 us with a CTA a row, 104 with rows
-// on their way and the weights read for each, 86 to 97 with the weights in registers; backward 292,
-// 148, 119 (two reductions a row instead of three, and the warps' sums added by shuffles).
+// on their way and the weights read for each, 86 to 98 with the weights in registers (by the GPU; 82 at the copy rate).  The
+// backward stays at those reductions' latency (one row on an SM at a time, DRAM at 59 %): 292, 148, 119 (two reductions a
+// row instead of three, and the warps' sums added by shuffles), 113 (a warp's lanes divide the sums); its few parts
+// of the sums take 11 us more to add, which is what few rows pay for (256 x 8192: 27 us, 3 at the copy rate).
 #include "la_common.cuh"
 #include "la_f32x2.cuh"
 

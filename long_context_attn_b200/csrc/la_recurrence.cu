@@ -17,11 +17,16 @@
 // warps.  A cluster's CTAs run at the same time, so every round arrives (the wait is bounded all the
 // same), and the result is the same in every run.
 //
-// What bounds it: instruction issue and its latencies, before memory (20 to 21 instructions an
-// element in bf16).  131072 x 8192 bf16 takes 1.46 ms, 4.4 TB/s of 6.56; backward of 8192 x 8192 146 us, 4.6
-// TB/s; 8192 x 8192 in fp32, half the elements a byte, 143 us, 5.7 TB/s.  Pairs of channels share an
+// What bounds it: latency, with few warps to hide it.  The rows that a thread keeps take 128 registers, so an SM
+// has 16 warps; 8192 x 8192 in bf16 is 24.4 instructions an element (the backward 40.8), which fill 57 % of the issue
+// slots, with DRAM at 49 %: of 3.2 warps on a scheduler 1.07 are ready, the others wait for a fixed latency, the shared-memory
+// and special-function queues, or the barrier.  131072 x 8192 bf16 takes 1.44 ms, 4.5 TB/s of 6.56; backward of 8192 x 8192 145 us,
+// 4.6 TB/s; 8192 x 8192 in fp32, half the elements a byte, 146 us, 5.5 TB/s.  Pairs of channels share an
 // instruction where the hardware has one; tiles in which a sequence starts or ends, which are few, run code of
-// their own, so that the others' has no tests (231 us with them at 16384 x 8192, 166 without).
+// their own, so that the others' has no tests (231 us with them at 16384 x 8192, 166 without).  In clusters a sixth of
+// the warps' time goes to waiting for a round's sums.
+// The time follows the fullest SM: 2^27 bf16 values take 277 us at 5120 channels (160 CTAs on 148 SMs), 173 at 8192, 152 at
+// 9472 (296 CTAs, two an SM), and 236 at 9504, where the 297th CTA starts when the others end.
 //
 // The backward walks time in reverse: with c_t = a_t (dout_t + c_{t+1}) what flows into the
 // state before row t, rows act on the c that enters them from behind as c -> A c + C with the same
