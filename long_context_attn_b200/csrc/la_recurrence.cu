@@ -982,7 +982,7 @@ la_status common_rec(RecArgs& p, la_dtype dt, la_input_mode mode, void* workspac
       {p.s0, states, false, backward ? kNever : kBegin}, {p.s1, states, true, kEndOfWalk},
       {p.ds1, states, false, kBegin}, {p.ds0, states, true, kEndOfWalk}, {p.ck, cks, !backward, kNever},
       {p.out, rows, true, kNever}, {p.dx, rows, true, kNever}, {p.df, rows, true, kNever},
-      {workspace, l.total, true, kNever}};
+      {workspace, l.total - (p.ck ? l.ck : 0), true, kNever}};   // room for checkpoints is not used where they are given
   for (const auto& w : args) {
     if (!w.written || !w.at) continue;
     for (const auto& t : args)

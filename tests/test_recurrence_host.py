@@ -181,8 +181,9 @@ def test_recurrence_entries_refuse_overlaps(lib):
         if torch.cuda.is_available():
             continue
         first = at["ds1" if backward else "s0"]
+        # the error record and the copy of the states: 256 bytes and 2 * 64 floats; then room for checkpoints, unused here
         for kw in ({}, {last: first}, {last: near(first, 16)}, {last: near(first, -256)}, dict(out=near(at["x"], rows)),
-                   dict(out=near(at["x"], -rows)), dict(x=at["f"])):
+                   dict(out=near(at["x"], -rows)), dict(x=at["f"]), dict(ck=near(WS, 768))):
             assert call(**kw) == 3, (packed, backward, kw)
 
 
