@@ -87,3 +87,44 @@ def test_malformed_offsets_are_found_in_the_callers_workspace(cuda_device):
             with pytest.raises(la.LightningAttnError) as err:
                 la.lightning_attn_check(ws)
             assert err.value.status == la.LA_ERR_DEVICE
+
+
+def _layer(torch, ag, x, r, w, b, cu):
+    """Norm, then the recurrence of its two halves: outputs, and gradients by fixed weights."""
+    y, s = ag.layer_norm(x, w, b, residual=r)
+    u, f = y.chunk(2, -1)
+    h, state = ag.gated_recurrence_varlen(u, f, cu)
+    d = torch.linspace(-1, 1, h.numel(), device=h.device).view(h.shape).to(h.dtype)
+    grads = torch.autograd.grad((h, s, state), (x, r, w, b), (d, torch.ones_like(s), torch.ones_like(state)))
+    return [t.detach() for t in (h, state, s, *grads)]
+
+
+def test_on_another_stream_and_captured(cuda_device):
+    """Forward and backward on a stream of their own, and captured into a graph that is replayed on new inputs: as on the
+    current stream."""
+    torch, la = _torch()
+    from long_context_attn_b200 import autograd as ag
+    rows, W = 1500, 200
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    data = [[torch.randn(s, device="cuda", generator=gen) for s in ((rows, W), (rows, W), (W,), (W,))] for _ in range(2)]
+    cu = torch.tensor([0, 700, 700, 701, rows], dtype=torch.int32, device="cuda")
+    leaf = lambda ts: [t.clone().requires_grad_(True) for t in ts]  # noqa: E731
+    want = [_layer(torch, ag, *leaf(ts), cu) for ts in data]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [_layer(torch, ag, *leaf(ts), cu) for ts in data]
+    side.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+    held = leaf(data[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _layer(torch, ag, *held, cu)
+    for ts, w in ((data[0], want[0]), (data[1], want[1]), (data[0], want[0])):
+        with torch.no_grad():
+            for t, v in zip(held, ts):
+                t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))

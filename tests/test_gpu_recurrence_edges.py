@@ -240,3 +240,50 @@ def test_malformed_offsets_without_rows(B, cuda_device):
         call(backward, zero, None, last)
         assert not last.any()
         la.lightning_attn_check(ws)
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 260), ("f32", 3)])
+def test_most_channels(dtype, T, cuda_device):
+    """2^22 channels, the most a call takes: 131072 blocks of them, rows 8 and 16 MB apart."""
+    torch, la = _torch()
+    x, f, d, s0, ds1 = _inputs(T, T, 1, 1 << 22, dtype)
+    _walk_and_compare(la, x, f, d, s0, ds1, [T], True, dtype)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_sequences(packed, cuda_device):
+    """300000 sequences of one token (packed: every third is empty), forward and backward, against the formulas: with one
+    token G = dout + dstate_out.  u = 2^-24: the state is a scan of one step (16u + 200u of its terms, as in the reference);
+    a gate is within (8 + |f|)u and |f| < 14 here, so keep G is within 22u + u + u, and a keep G (h - x) within 44u and five
+    roundings more."""
+    torch, la = _torch()
+    B, W = 300000, 24
+    lens = np.ones(B, dtype=np.int64)
+    if packed:
+        lens[::3] = 0
+    rows = int(lens.sum())
+    x, f, d, s0, ds1 = _inputs(B, rows, B, W, "f32")
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+    ws = _ws(la, B, rows, W, x, True)
+    out, dx, df = (torch.full_like(x, float("nan")) for _ in range(3))
+    s1, ds0 = (torch.full_like(s0, float("nan")) for _ in range(2))
+    if packed:
+        la.lightning_attn_gated_recurrence_varlen(x, f, out, cu, s0, s1, workspace=ws)
+        la.lightning_attn_gated_recurrence_backward_varlen(x, f, d, dx, df, cu, s0, ds1, ds0, workspace=ws)
+    else:
+        v = lambda t: t.view(B, 1, W)  # noqa: E731
+        la.lightning_attn_gated_recurrence(v(x), v(f), v(out), s0, s1, workspace=ws)
+        la.lightning_attn_gated_recurrence_backward(v(x), v(f), v(d), v(dx), v(df), s0, ds1, ds0, workspace=ws)
+    la.lightning_attn_check(ws)
+    some = lens > 0
+    a64, x64, d64, s64, g64 = ref.sigmoid(_np(f)), _np(x), _np(d), _np(s0)[some], _np(ds1)[some]
+    keep = ref.sigmoid(-_np(f))
+    h, tol = a64 * s64 + keep * x64, 216 * ref.U * (np.abs(a64 * s64) + np.abs(keep * x64))
+    ref.check("out", _np(out), h, tol)
+    ref.check("state_out", _np(s1)[some], h, tol)
+    G, Gabs = d64 + g64, np.abs(d64) + np.abs(g64)
+    ref.check("dx", _np(dx), keep * G, 32 * ref.U * keep * Gabs)
+    ref.check("df", _np(df), a64 * keep * G * (s64 - x64), 64 * ref.U * a64 * keep * Gabs * (np.abs(s64) + np.abs(x64)))
+    ref.check("dstate_in", _np(ds0)[some], a64 * G, 216 * ref.U * a64 * Gabs)
+    assert torch.equal(s1[torch.from_numpy(~some).cuda()], s0[torch.from_numpy(~some).cuda()])
+    assert torch.equal(ds0[torch.from_numpy(~some).cuda()], ds1[torch.from_numpy(~some).cuda()])
